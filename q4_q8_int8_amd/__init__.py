@@ -1,7 +1,8 @@
 """q4_K x q8_1 quantized matrix multiply (MMQ) on MI355X (gfx950).
 
 A thin ctypes binding over libmmq.so, whose C ABI is declared in include/mmq.h (the integer
-product) and include/mmq_f16.h (the f16 comparator path). The functions here have the same
+product), include/mmq_layer.h (its epilogue, the gated product, the mixture-of-experts layer) and
+include/mmq_f16.h (the f16 comparator path). The functions here have the same
 names and arguments as the C entry points and only marshal arguments: each tensor is checked
 (a contiguous CUDA tensor on the current device, of the expected dtype and at least the size
 the call reads or writes; MMQArgumentError otherwise) and passed as a device pointer, the
@@ -19,7 +20,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmmq.so")
 INCLUDE_DIR = os.path.join(os.path.dirname(_PKG), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "mmq.h")
-HEADER_PATHS = (HEADER_PATH, os.path.join(INCLUDE_DIR, "mmq_f16.h"))
+HEADER_PATHS = (HEADER_PATH, os.path.join(INCLUDE_DIR, "mmq_layer.h"),
+                os.path.join(INCLUDE_DIR, "mmq_f16.h"))
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python q4_q8_int8_amd/build.py`")
@@ -40,6 +42,15 @@ MMQ_OK, MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP = range(6)
 GEMV_MAX_M = 16  # largest M of the decode tile, which the guard chooses up to there
 QK8, QK_K, Q4K_BLOCK_BYTES, REP_TILE_ROWS, REP_TILE_BYTES = 32, 256, 144, 32, 4608
 Q6K_BLOCK_BYTES, REP6_TILE_BYTES = 210, 10240
+(MMQ_ACT_NONE, MMQ_ACT_RELU, MMQ_ACT_SILU, MMQ_ACT_GELU, MMQ_ACT_GELU_TANH) = range(5)
+ACTIVATIONS = {"none": MMQ_ACT_NONE, "relu": MMQ_ACT_RELU, "silu": MMQ_ACT_SILU,
+               "gelu": MMQ_ACT_GELU, "gelu_tanh": MMQ_ACT_GELU_TANH}
+MMQ_SCORE_SOFTMAX, MMQ_SCORE_SIGMOID = range(2)
+SCORES = {"softmax": MMQ_SCORE_SOFTMAX, "sigmoid": MMQ_SCORE_SIGMOID}
+MOE_MAX_TOKENS, MOE_MAX_PAIRS, MOE_MAX_EXPERTS, MOE_MAX_SLOTS = 64, 512, 512, 64
+# up to this many tokens the products from float32 activations (mmq_q4K_f32 and its forms) beat
+# quantize_q8_1 followed by the product
+FUSED_TOKENS = 4
 
 
 class mmq_options(ctypes.Structure):
@@ -61,6 +72,11 @@ class mmq_kernel_info(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class mmq_epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class MMQError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -70,6 +86,7 @@ class MMQError(RuntimeError):
 
 
 _i64, _vp, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+_i32c = ctypes.c_int32
 _SIGS = {
     "mmq_q8_1_bytes": [_i64, _i64, ctypes.POINTER(_sz)],
     "mmq_q4K_bytes": [_i64, _i64, ctypes.POINTER(_sz)],
@@ -93,6 +110,23 @@ _SIGS = {
     "mmq_plan": [_i64, _i64, _i64, ctypes.POINTER(mmq_options), _i64,
                  ctypes.POINTER(mmq_kernel_info)],
     "mmq_last_kernel": [ctypes.POINTER(mmq_kernel_info)],
+    "mmq_q4K_q8_1_epilogue": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.POINTER(mmq_epilogue),
+                              ctypes.POINTER(mmq_options)],
+    "mmq_q4K_f32_epilogue": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, ctypes.POINTER(mmq_epilogue)],
+    "mmq_q4K_pair_bytes": [_i64, _i64, ctypes.POINTER(_sz)],
+    "repack_q4_K_pair": [_vp, _vp, _i64, _i64, _vp, _vp],
+    "mmq_gated_workspace_bytes": [_i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_q4K_q8_1_gated": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32c,
+                           ctypes.POINTER(mmq_options)],
+    "mmq_q4K_f32_gated": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32c],
+    "mmq_moe_plan_bytes": [_i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_moe_plan": [_i64, _i64, _i64, _vp, _vp, _vp],
+    "mmq_moe_route": [_i64, _i64, _i64, _vp, _i32c, _i32c, _vp, _vp, _vp, _vp],
+    "mmq_q4K_moe_gated": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32c, _vp],
+    "mmq_q4K_moe_down": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "mmq_moe_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_q4K_moe": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _i32c, _i32c, _vp, _i32c, _vp, _vp,
+                    _vp, _vp, _sz, _vp],
     "mmq_f16_bytes": [_i64, _i64, ctypes.POINTER(_sz)],
     "convert_f32_f16": [_vp, _i64, _i64, _vp, _vp],
     "dequantize_q4_K_f16": [_vp, _i64, _i64, _vp, _vp],
@@ -107,7 +141,7 @@ for _name, _args in _SIGS.items():
 
 
 def exported_symbols() -> list[str]:
-    """Function names declared in the library's headers (include/mmq.h, include/mmq_f16.h)."""
+    """Function names declared in the library's headers (include/*.h)."""
     names = []
     for path in HEADER_PATHS:
         with open(path) as f:
@@ -280,6 +314,164 @@ def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
     _check("mmq_q4K_q8_1_blockdots",
            _lib.mmq_q4K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp,
                                        _stream(stream), _opts(force_tile, lds_budget)))
+
+
+# ---------------------------------------------------------------- the product's epilogue
+def _epi(M: int, N: int, bias, residual, act: int):
+    bp = None if bias is None else _dev(bias, "bias", 4 * N, _f32())
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * N, _f32())
+    return ctypes.byref(mmq_epilogue(bp, rp, act, 0))
+
+
+def mmq_q4K_q8_1_epilogue(M: int, N: int, K: int, q8, w_rep, C, bias=None, residual=None,
+                          act: int = MMQ_ACT_NONE, stream=None, force_tile: int = MMQ_TILE_AUTO,
+                          lds_budget: int = 0, min_workgroups: int = 0, workspace=None,
+                          splits: int = 0) -> None:
+    """C[M, N] = act(product + bias[N]) + residual[M, N] (f32 tensors; residual may be C)."""
+    qp, rp, cp = _gemm_ptrs(M, N, K, q8, w_rep, C)
+    wp, wb = _workspace(workspace)
+    _check("mmq_q4K_q8_1_epilogue",
+           _lib.mmq_q4K_q8_1_epilogue(M, N, K, qp, rp, cp, _stream(stream),
+                                      _epi(M, N, bias, residual, act),
+                                      _opts(force_tile, lds_budget, min_workgroups, wp, wb,
+                                            splits)))
+
+
+def mmq_q4K_f32_epilogue(M: int, N: int, K: int, x, w_rep, C, bias=None, residual=None,
+                         act: int = MMQ_ACT_NONE, stream=None) -> None:
+    """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
+    xp = _dev(x, "x", 4 * M * K, _f32())
+    rp = _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K))
+    cp = _dev(C, "C", 4 * M * N, _f32())
+    _check("mmq_q4K_f32_epilogue",
+           _lib.mmq_q4K_f32_epilogue(M, N, K, xp, rp, cp, _stream(stream),
+                                     _epi(M, N, bias, residual, act)))
+
+
+# ---------------------------------------------------------------- the gated product
+def mmq_q4K_pair_bytes(F: int, K: int) -> int:
+    n = _sz()
+    _check("mmq_q4K_pair_bytes", _lib.mmq_q4K_pair_bytes(F, K, ctypes.byref(n)))
+    return n.value
+
+
+def repack_q4_K_pair(w_gate, w_up, F: int, K: int, w_pair, stream=None) -> None:
+    """w_gate, w_up: q4_K blocks (mmq_q4K_bytes(F, K)); w_pair: mmq_q4K_pair_bytes(F, K) bytes."""
+    gp = _dev(w_gate, "w_gate", mmq_q4K_bytes(F, K))
+    up = _dev(w_up, "w_up", mmq_q4K_bytes(F, K))
+    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    _check("repack_q4_K_pair", _lib.repack_q4_K_pair(gp, up, F, K, pp, _stream(stream)))
+
+
+def mmq_gated_workspace_bytes(M: int, F: int, K: int) -> int:
+    """Split-K workspace mmq_q4K_q8_1_gated would use given an unlimited one (0: none)."""
+    n = _sz()
+    _check("mmq_gated_workspace_bytes",
+           _lib.mmq_gated_workspace_bytes(M, F, K, ctypes.byref(n)))
+    return n.value
+
+
+def mmq_q4K_q8_1_gated(M: int, F: int, K: int, q8, w_pair, H, act: int = MMQ_ACT_SILU,
+                       stream=None, force_tile: int = MMQ_TILE_AUTO, lds_budget: int = 0,
+                       min_workgroups: int = 0, workspace=None, splits: int = 0) -> None:
+    """H[M, F] (f32) = act(x Wg^T) * (x Wu^T), q8 (M x K) and a repacked pair (F x K)."""
+    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, K))
+    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    hp = _dev(H, "H", 4 * M * F, _f32())
+    wp, wb = _workspace(workspace)
+    _check("mmq_q4K_q8_1_gated",
+           _lib.mmq_q4K_q8_1_gated(M, F, K, qp, pp, hp, _stream(stream), act,
+                                   _opts(force_tile, lds_budget, min_workgroups, wp, wb, splits)))
+
+
+def mmq_q4K_f32_gated(M: int, F: int, K: int, x, w_pair, H, act: int = MMQ_ACT_SILU,
+                      stream=None) -> None:
+    """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
+    xp = _dev(x, "x", 4 * M * K, _f32())
+    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    hp = _dev(H, "H", 4 * M * F, _f32())
+    _check("mmq_q4K_f32_gated",
+           _lib.mmq_q4K_f32_gated(M, F, K, xp, pp, hp, _stream(stream), act))
+
+
+# ---------------------------------------------------------------- mixture of experts
+def mmq_moe_plan_bytes(M: int, E: int, k: int) -> int:
+    n = _sz()
+    _check("mmq_moe_plan_bytes", _lib.mmq_moe_plan_bytes(M, E, k, ctypes.byref(n)))
+    return n.value
+
+
+def mmq_moe_plan(M: int, E: int, k: int, ids, plan, stream=None) -> None:
+    """plan (int32, mmq_moe_plan_bytes) from ids int32 [M, k]; an id outside [0, E) is no expert."""
+    ip = _dev(ids, "ids", 4 * M * k, _i32())
+    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    _check("mmq_moe_plan", _lib.mmq_moe_plan(M, E, k, ip, pp, _stream(stream)))
+
+
+def mmq_moe_route(M: int, E: int, k: int, logits, ids, weights, plan=None,
+                  score: int = MMQ_SCORE_SOFTMAX, renorm: bool = True, stream=None) -> None:
+    """The k experts of the greatest logits [M, E] (f32): ids int32 [M, k], weights f32 [M, k] and,
+    for at most 64 tokens, the plan of the experts' products (int32, mmq_moe_plan_bytes)."""
+    lp = _dev(logits, "logits", 4 * M * E, _f32())
+    ip = _dev(ids, "ids", 4 * M * k, _i32())
+    wp = _dev(weights, "weights", 4 * M * k, _f32())
+    pp = None if plan is None else _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    _check("mmq_moe_route",
+           _lib.mmq_moe_route(M, E, k, lp, score, int(renorm), ip, wp, pp, _stream(stream)))
+
+
+def mmq_q4K_moe_gated(M: int, E: int, k: int, F: int, D: int, x, plan, w_pairs, H, q8,
+                      act: int = MMQ_ACT_SILU, stream=None) -> None:
+    """H[M*k, F] (f32): per (token, slot) pair of the plan the gated product of its expert.
+    w_pairs: E repacked pairs (mmq_q4K_pair_bytes(F, D) each); q8: scratch, mmq_q8_1_bytes(M, D)."""
+    xp = _dev(x, "x", 4 * M * D, _f32())
+    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    wp = _dev(w_pairs, "w_pairs", E * mmq_q4K_pair_bytes(F, D))
+    hp = _dev(H, "H", 4 * M * k * F, _f32())
+    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, D))
+    _check("mmq_q4K_moe_gated",
+           _lib.mmq_q4K_moe_gated(M, E, k, F, D, xp, pp, wp, hp, qp, act, _stream(stream)))
+
+
+def mmq_q4K_moe_down(M: int, E: int, k: int, D: int, F: int, H, plan, weights, w_down, out, q8,
+                     residual=None, stream=None) -> None:
+    """out[M, D] (f32) = residual + per token the weighted sum over its slots of H[p] W(expert)^T.
+    w_down: E repacked matrices (mmq_q4K_repacked_bytes(D, F) each); q8: scratch of
+    mmq_q8_1_bytes(M*k, F) bytes; residual may be out."""
+    hp = _dev(H, "H", 4 * M * k * F, _f32())
+    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    gp = _dev(weights, "weights", 4 * M * k, _f32())
+    wp = _dev(w_down, "w_down", E * mmq_q4K_repacked_bytes(D, F))
+    op = _dev(out, "out", 4 * M * D, _f32())
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
+    qp = _dev(q8, "q8", mmq_q8_1_bytes(M * k, F))
+    _check("mmq_q4K_moe_down",
+           _lib.mmq_q4K_moe_down(M, E, k, D, F, hp, pp, gp, wp, rp, op, qp, _stream(stream)))
+
+
+def mmq_moe_workspace_bytes(M: int, E: int, k: int, D: int, F: int) -> int:
+    n = _sz()
+    _check("mmq_moe_workspace_bytes",
+           _lib.mmq_moe_workspace_bytes(M, E, k, D, F, ctypes.byref(n)))
+    return n.value
+
+
+def mmq_q4K_moe(M: int, E: int, k: int, D: int, F: int, x, logits, w_pairs, w_down, out,
+                workspace, score: int = MMQ_SCORE_SOFTMAX, renorm: bool = True,
+                act: int = MMQ_ACT_SILU, residual=None, stream=None) -> None:
+    """The whole layer for a few tokens: out[M, D] = residual + experts of x [M, D] chosen by the
+    router's logits [M, E]. workspace: mmq_moe_workspace_bytes(M, E, k, D, F) bytes."""
+    xp = _dev(x, "x", 4 * M * D, _f32())
+    lp = _dev(logits, "logits", 4 * M * E, _f32())
+    gp = _dev(w_pairs, "w_pairs", E * mmq_q4K_pair_bytes(F, D))
+    dp = _dev(w_down, "w_down", E * mmq_q4K_repacked_bytes(D, F))
+    op = _dev(out, "out", 4 * M * D, _f32())
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
+    sp, sb = _dev(workspace, "workspace", mmq_moe_workspace_bytes(M, E, k, D, F)), \
+        workspace.numel() * workspace.element_size()
+    _check("mmq_q4K_moe",
+           _lib.mmq_q4K_moe(M, E, k, D, F, xp, lp, score, int(renorm), gp, act, dp, rp, op, sp, sb,
+                            _stream(stream)))
 
 
 # ---------------------------------------------------------------- the q6_K variant

@@ -13,6 +13,7 @@
 
 #include "mmq.h"
 #include "mmq_f16.h"
+#include "mmq_layer.h"
 #include "mmq_internal.h"
 
 namespace {
@@ -346,25 +347,30 @@ int check_gemm_call(int64_t M, int64_t N, int64_t K, const void* q8, const void*
 // a second kernel adds them into C, both on the stream.
 int launch_planned(const mmq_kernel_info& info, int64_t M, int64_t N, int64_t K, const void* q8,
                    const void* w_rep, float* C, void* ws, int64_t compute_units,
-                   hipStream_t stream, int fmt = mmq::kFmtQ4K) {
+                   hipStream_t stream, int fmt = mmq::kFmtQ4K,
+                   const mmq::Epilogue& epi = mmq::Epilogue{}) {
   hipError_t e;
   if (info.tile == MMQ_TILE_GEMV) {
     // the form the guard chose: the matrix-unit form takes all tokens in one workgroup, with
     // threads / 64 wavefronts and block_n weight rows
     e = mmq::launch_mmq_gemv(q8, w_rep, C, M, N, K,
                              info.block_m == mmq::kGemvMaxM ? info.threads / 64 : 0,
-                             info.block_n, stream);
+                             info.block_n, stream, epi);
   } else if (info.tile == MMQ_TILE_SKINNY) {
-    e = mmq::launch_mmq_skinny(q8, w_rep, C, M, N, K, compute_units, stream);
+    e = mmq::launch_mmq_skinny(q8, w_rep, C, M, N, K, compute_units, stream, epi);
   } else {
     const mmq::TileShape ts = tile_shape(info.tile);
     const int64_t gm = (M + ts.block_m() - 1) / ts.block_m();
     const int64_t gn = ((N + 31) / 32 + ts.nw - 1) / ts.nw;
     const int64_t sp = info.splits;
-    e = mmq::launch_mmq(info.tile, q8, w_rep, sp > 1 ? ws : C, M, N, K, gm, gn, sp, 0, 0, false,
-                        0, 0, 0, 0, stream, fmt);
+    // with split-K the partial planes are plain sums, and the second kernel has the epilogue
+    if (sp == 1 && epi.kind != mmq::kEpiNone)
+      e = mmq::launch_mmq_epilogue(info.tile, q8, w_rep, C, M, N, K, gm, gn, epi, stream);
+    else
+      e = mmq::launch_mmq(info.tile, q8, w_rep, sp > 1 ? ws : C, M, N, K, gm, gn, sp, 0, 0, false,
+                          0, 0, 0, 0, stream, fmt);
     if (e == hipSuccess && sp > 1)
-      e = mmq::launch_reduce_splits(static_cast<const float*>(ws), C, M, N, sp, stream);
+      e = mmq::launch_reduce_splits(static_cast<const float*>(ws), C, M, N, sp, stream, epi);
   }
   if (e != hipSuccess) return hip_fail("mmq_q4K_q8_1 launch", e);
   return ok();
@@ -372,7 +378,8 @@ int launch_planned(const mmq_kernel_info& info, int64_t M, int64_t N, int64_t K,
 
 // The GEMM entry points of both weight formats: validate, plan, launch.
 int gemm_ex(int fmt, int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
-            float* C, void* stream, const mmq_options* opt) {
+            float* C, void* stream, const mmq_options* opt,
+            const mmq::Epilogue& epi = mmq::Epilogue{}) {
   int st = check_gemm_call(M, N, K, q8, w_rep, C, opt);
   if (st) return st;
   if (opt && opt->workspace_bytes > 0 && (!opt->workspace || !aligned16(opt->workspace)))
@@ -384,7 +391,86 @@ int gemm_ex(int fmt, int64_t M, int64_t N, int64_t K, const void* q8, const void
   g_last = info;
   if (st) return st;
   return launch_planned(info, M, N, K, q8, w_rep, C, opt ? opt->workspace : nullptr,
-                        di->compute_units, static_cast<hipStream_t>(stream), fmt);
+                        di->compute_units, static_cast<hipStream_t>(stream), fmt, epi);
+}
+
+// mmq_q4K_f32 and its forms with an epilogue.
+int gemm_f32(const char* fn, int64_t M, int64_t N, int64_t K, const float* x, const void* w_rep,
+             float* C, void* stream, const mmq::Epilogue& epi = mmq::Epilogue{}) {
+  int st = check_gemm_shape(M, N, K);
+  if (st) return st;
+  if (M > kFusedMaxM)
+    return fail(MMQ_E_SHAPE, "%s is for few tokens: M = %lld is above %lld", fn, (long long)M,
+                (long long)kFusedMaxM);
+  if (!x || !w_rep || !C) return fail(MMQ_E_ARG, "null device pointer");
+  if (!aligned16(x) || !aligned16(w_rep) || !aligned16(C))
+    return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");
+  DeviceInfo* di;
+  if ((st = current_device(&di))) return st;
+  // up to kGemvFusedMaxM tokens the vector-ALU kernel, else the skinny one, each quantizing
+  // the activations itself
+  const bool gemv = M <= mmq::kGemvFusedMaxM;
+  mmq_kernel_info info = {};
+  info.reason = MMQ_REASON_FUSED;
+  info.lds_budget = di->lds_budget;
+  if (gemv) {
+    info.tile = MMQ_TILE_GEMV;
+    info.block_m = (int32_t)mmq::gemv_group(M, 0);
+    info.block_n = mmq::kGemvRows;
+    info.threads = 64 * mmq::kGemvWaves;
+    info.lds_bytes = mmq::gemv_lds_bytes(M, 0, mmq::kGemvRows);
+    info.grid = mmq::gemv_grid(M, N, 0, mmq::kGemvRows);
+  } else {
+    info.tile = MMQ_TILE_SKINNY;
+    info.block_m = 32;
+    info.block_n = 32;
+    info.threads = 64 * mmq::kSkinnyWaves;
+    info.lds_bytes = mmq::fused_lds_bytes();
+    info.grid = ((M + 31) / 32) * ((N + 31) / 32);
+  }
+  if (info.lds_bytes > di->lds_budget) {
+    info.tile = MMQ_TILE_AUTO;
+    info.reason = MMQ_REASON_NO_FIT;
+    g_last = info;
+    return fail(MMQ_E_LDS, "%s needs %lld bytes of LDS, the device allows %lld", fn,
+                (long long)info.lds_bytes, (long long)di->lds_budget);
+  }
+  g_last = info;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = gemv ? mmq::launch_mmq_gemv_fused(x, w_rep, C, M, N, K, s, epi)
+                      : mmq::launch_mmq_fused(x, w_rep, C, M, N, K, s, epi);
+  if (e != hipSuccess) return fail(MMQ_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return ok();
+}
+
+// The caller's epilogue, checked, as the launchers take it.
+int make_epilogue(const mmq_epilogue* epi, mmq::Epilogue* out) {
+  *out = mmq::Epilogue{};
+  if (!epi) return MMQ_OK;
+  if (epi->act < MMQ_ACT_NONE || epi->act > MMQ_ACT_GELU_TANH)
+    return fail(MMQ_E_ARG, "act %d is not an mmq_act", epi->act);
+  if (epi->reserved != 0) return fail(MMQ_E_ARG, "mmq_epilogue.reserved must be 0");
+  if (!aligned16(epi->bias) || !aligned16(epi->residual))
+    return fail(MMQ_E_ARG, "bias and residual must be 16-byte aligned");
+  if (!epi->bias && !epi->residual && epi->act == MMQ_ACT_NONE) return MMQ_OK;
+  out->kind = mmq::kEpiAct;
+  out->act = epi->act;
+  out->bias = epi->bias;
+  out->residual = epi->residual;
+  return MMQ_OK;
+}
+
+// The gated product's epilogue; checks F so that the packed row count stays in range.
+int make_gated(int64_t F, int32_t act, mmq::Epilogue* out) {
+  if (F <= 0) return fail(MMQ_E_ARG, "F must be positive (%lld)", (long long)F);
+  if (F > kMaxDim / 2) return fail(MMQ_E_SHAPE, "F above 2^29");
+  if (act < MMQ_ACT_NONE || act > MMQ_ACT_GELU_TANH)
+    return fail(MMQ_E_ARG, "act %d is not an mmq_act", act);
+  *out = mmq::Epilogue{};
+  out->kind = mmq::kEpiGated;
+  out->act = act;
+  out->F = F;
+  return MMQ_OK;
 }
 
 int blockdots(int fmt, int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
@@ -446,6 +532,13 @@ int api_current_device() {
   DeviceInfo* di;
   return current_device(&di);
 }
+int api_current_device(int64_t* lds_budget) {
+  DeviceInfo* di;
+  const int st = current_device(&di);
+  if (!st) *lds_budget = di->lds_budget;
+  return st;
+}
+int api_ok() { return ok(); }
 }  // namespace mmq
 
 extern "C" {
@@ -547,56 +640,78 @@ int mmq_q4K_q8_1(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_
 
 int mmq_q4K_f32(int64_t M, int64_t N, int64_t K, const float* x, const void* w_rep, float* C,
                 void* stream) {
-  int st = check_gemm_shape(M, N, K);
-  if (st) return st;
-  if (M > kFusedMaxM)
-    return fail(MMQ_E_SHAPE, "mmq_q4K_f32 is for few tokens: M = %lld is above %lld",
-                (long long)M, (long long)kFusedMaxM);
-  if (!x || !w_rep || !C) return fail(MMQ_E_ARG, "null device pointer");
-  if (!aligned16(x) || !aligned16(w_rep) || !aligned16(C))
-    return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");
-  DeviceInfo* di;
-  if ((st = current_device(&di))) return st;
-  // up to kGemvFusedMaxM tokens the vector-ALU kernel, else the skinny one, each quantizing
-  // the activations itself
-  const bool gemv = M <= mmq::kGemvFusedMaxM;
-  mmq_kernel_info info = {};
-  info.reason = MMQ_REASON_FUSED;
-  info.lds_budget = di->lds_budget;
-  if (gemv) {
-    info.tile = MMQ_TILE_GEMV;
-    info.block_m = (int32_t)mmq::gemv_group(M, 0);
-    info.block_n = mmq::kGemvRows;
-    info.threads = 64 * mmq::kGemvWaves;
-    info.lds_bytes = mmq::gemv_lds_bytes(M, 0, mmq::kGemvRows);
-    info.grid = mmq::gemv_grid(M, N, 0, mmq::kGemvRows);
-  } else {
-    info.tile = MMQ_TILE_SKINNY;
-    info.block_m = 32;
-    info.block_n = 32;
-    info.threads = 64 * mmq::kSkinnyWaves;
-    info.lds_bytes = mmq::fused_lds_bytes();
-    info.grid = ((M + 31) / 32) * ((N + 31) / 32);
-  }
-  if (info.lds_bytes > di->lds_budget) {
-    info.tile = MMQ_TILE_AUTO;
-    info.reason = MMQ_REASON_NO_FIT;
-    g_last = info;
-    return fail(MMQ_E_LDS, "mmq_q4K_f32 needs %lld bytes of LDS, the device allows %lld",
-                (long long)info.lds_bytes, (long long)di->lds_budget);
-  }
-  g_last = info;
-  hipError_t e = gemv ? mmq::launch_mmq_gemv_fused(x, w_rep, C, M, N, K,
-                                                   static_cast<hipStream_t>(stream))
-                      : mmq::launch_mmq_fused(x, w_rep, C, M, N, K, static_cast<hipStream_t>(stream));
-  if (e != hipSuccess) return hip_fail("mmq_q4K_f32 launch", e);
-  return ok();
+  return gemm_f32("mmq_q4K_f32", M, N, K, x, w_rep, C, stream);
 }
 
 int mmq_q4K_q8_1_blockdots(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
                            int64_t i0, int64_t i1, int64_t j0, int64_t j1, int32_t* S,
                            void* stream, const mmq_options* opt) {
   return blockdots(mmq::kFmtQ4K, M, N, K, q8, w_rep, i0, i1, j0, j1, S, stream, opt);
+}
+
+// ---------------------------------------------------------------- the product's epilogue
+
+int mmq_q4K_q8_1_epilogue(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
+                          float* C, void* stream, const mmq_epilogue* epi,
+                          const mmq_options* opt) {
+  mmq::Epilogue e;
+  const int st = make_epilogue(epi, &e);
+  return st ? st : gemm_ex(mmq::kFmtQ4K, M, N, K, q8, w_rep, C, stream, opt, e);
+}
+
+int mmq_q4K_f32_epilogue(int64_t M, int64_t N, int64_t K, const float* x, const void* w_rep,
+                         float* C, void* stream, const mmq_epilogue* epi) {
+  mmq::Epilogue e;
+  const int st = make_epilogue(epi, &e);
+  return st ? st : gemm_f32("mmq_q4K_f32_epilogue", M, N, K, x, w_rep, C, stream, e);
+}
+
+int mmq_q4K_pair_bytes(int64_t F, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(MMQ_E_ARG, "bytes is NULL");
+  if (F <= 0 || K <= 0) return fail(MMQ_E_ARG, "F and K must be positive");
+  if (F > kMaxDim / 2) return fail(MMQ_E_SHAPE, "weight matrix too large");
+  return mmq_q4K_repacked_bytes(mmq::pair_rows(F), K, bytes);
+}
+
+int repack_q4_K_pair(const void* w_gate, const void* w_up, int64_t F, int64_t K, void* w_pair,
+                     void* stream) {
+  size_t nb;
+  int st = mmq_q4K_pair_bytes(F, K, &nb);
+  if (st) return st;
+  if ((__int128)((F + 15) / 16) * (K / MMQ_QK_K) >= ((__int128)1 << 31))
+    return fail(MMQ_E_SHAPE, "repack_q4_K_pair takes ceil(F/16)*(K/256) below 2^31");
+  if (!w_gate || !w_up || !w_pair) return fail(MMQ_E_ARG, "null device pointer");
+  if (!aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_pair))
+    return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");
+  DeviceInfo* di;
+  if ((st = current_device(&di))) return st;
+  hipError_t e =
+      mmq::launch_repack_q4_K_pair(w_gate, w_up, F, K, w_pair, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail("repack_q4_K_pair launch", e);
+  return ok();
+}
+
+int mmq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t* bytes) {
+  if (!bytes) return fail(MMQ_E_ARG, "bytes is NULL");
+  mmq::Epilogue e;
+  const int st = make_gated(F, MMQ_ACT_NONE, &e);
+  return st ? st : mmq_workspace_bytes(M, mmq::pair_rows(F), K, bytes);
+}
+
+int mmq_q4K_q8_1_gated(int64_t M, int64_t F, int64_t K, const void* q8, const void* w_pair,
+                       float* H, void* stream, int32_t act, const mmq_options* opt) {
+  mmq::Epilogue e;
+  const int st = make_gated(F, act, &e);
+  return st ? st
+            : gemm_ex(mmq::kFmtQ4K, M, mmq::pair_rows(F), K, q8, w_pair, H, stream, opt, e);
+}
+
+int mmq_q4K_f32_gated(int64_t M, int64_t F, int64_t K, const float* x, const void* w_pair,
+                      float* H, void* stream, int32_t act) {
+  mmq::Epilogue e;
+  const int st = make_gated(F, act, &e);
+  return st ? st
+            : gemm_f32("mmq_q4K_f32_gated", M, mmq::pair_rows(F), K, x, w_pair, H, stream, e);
 }
 
 // ---------------------------------------------------------------- q6_K

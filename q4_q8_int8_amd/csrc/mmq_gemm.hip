@@ -49,6 +49,7 @@
 // On gfx950 the MFMA and the vector ALU of a SIMD largely take turns, so every instruction
 // counts: the rescale is 2 FMAs per element-block and the int8 MFMA of step n+1 is issued
 // before the rescale of step n.
+#include "epilogue.h"
 #include "mmq_device.h"
 
 namespace mmq {
@@ -62,12 +63,15 @@ __device__ __forceinline__ void set_priority(int p) {
   else __builtin_amdgcn_s_setprio(0);
 }
 
-template <int TT, int NW, bool STORE_S, int FMT>
+// EPI: the epilogue (epilogue.h). kEpiGated: N counts packed rows (pair_rows(F)) and the output is
+// H[M][F]; there is then one split.
+template <int TT, int NW, bool STORE_S, int FMT, int EPI>
 __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
     const int8_t* __restrict__ qs, const float* __restrict__ da_plane,
     const uint16_t* __restrict__ tpieces,
     const uint8_t* __restrict__ wrep, void* __restrict__ out, int M, int N, int K, int gm,
-    int gmn, int splits, int tm0, int tn0, int i0, int i1, int j0, int j1, int xbm, int xgm) {
+    int gmn, int splits, int tm0, int tn0, int i0, int i1, int j0, int j1, int xbm, int xgm,
+    EpiParam<EPI> epi) {
   constexpr int BM = 32 * TT;
   constexpr int NS = 8 * TT;                      // (block, token tile) steps per super-block
   constexpr int A_BYTES = BM * kRowStride;        // token tile
@@ -450,7 +454,50 @@ __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
     }
   }
 
-  if constexpr (!STORE_S) {
+  if constexpr (!STORE_S && EPI == kEpiGated) {
+    // Registers 8 c .. 8 c + 3 of a lane are the gate rows 4 h .. 4 h + 3 of the tile's packed
+    // 16-row half c and registers 8 c + 4 .. 8 c + 7 the same up rows: the lane forms 8 columns
+    // of H for its token, and the tile's 16 columns go out through the LDS transpose of the
+    // plain epilogue (below), four lanes to a token row's 64 bytes.
+    constexpr int TS = 20;
+    float* H = static_cast<float*>(out);
+    const int F = epi.F;
+    const int rr = lane >> 2, c4 = lane & 3;  // read-back: rows rr + 16 k, columns 4*c4..+3
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      float* tile = reinterpret_cast<float*>(smem) + ((t & 1) * NW + wave) * (32 * TS);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[r] = activate(acc[t][8 * c + r], epi.act) * acc[t][8 * c + 4 + r];
+        *reinterpret_cast<float4*>(tile + l32 * TS + 8 * c + 4 * h) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (wt_ok) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int row = rr + 16 * k;
+          const int i = m0 + t * 32 + row;
+          const int j = wt * 16 + 4 * c4;
+          if (i >= M) continue;
+          const float4 v = *reinterpret_cast<const float4*>(tile + row * TS + 4 * c4);
+          float* p = H + (size_t)i * F + j;
+          if ((F & 3) == 0 && j + 3 < F) {
+            *reinterpret_cast<float4*>(p) = v;
+          } else {
+            if (j + 0 < F) p[0] = v.x;
+            if (j + 1 < F) p[1] = v.y;
+            if (j + 2 < F) p[2] = v.z;
+            if (j + 3 < F) p[3] = v.w;
+          }
+        }
+      }
+    }
+  } else if constexpr (!STORE_S) {
     // Output tile by tile through LDS (the stage buffers are free now: every wavefront has
     // passed the last stage's barrier): lane (l32, h) holds 16 columns of one token row, which
     // would make every store instruction touch 64 rows; after the transpose 8 consecutive
@@ -480,14 +527,15 @@ __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
           const int j = j0c + 4 * c4;
           if (i >= M) continue;
           const float4 v = *reinterpret_cast<const float4*>(tile + row * TS + 4 * c4);
-          float* p = C + (size_t)i * N + j;
+          const size_t at = (size_t)i * N + j;
+          float* p = C + at;
           if ((N & 3) == 0 && j + 3 < N) {
-            *reinterpret_cast<float4*>(p) = v;
+            *reinterpret_cast<float4*>(p) = epi_four<EPI>(epi, v, at, j);
           } else {
-            if (j + 0 < N) p[0] = v.x;
-            if (j + 1 < N) p[1] = v.y;
-            if (j + 2 < N) p[2] = v.z;
-            if (j + 3 < N) p[3] = v.w;
+            if (j + 0 < N) p[0] = epi_one<EPI>(epi, v.x, at, j);
+            if (j + 1 < N) p[1] = epi_one<EPI>(epi, v.y, at + 1, j + 1);
+            if (j + 2 < N) p[2] = epi_one<EPI>(epi, v.z, at + 2, j + 2);
+            if (j + 3 < N) p[3] = epi_one<EPI>(epi, v.w, at + 3, j + 3);
           }
         }
       }
@@ -495,17 +543,18 @@ __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
   }
 }
 
-template <int TT, int NW, bool STORE_S, int FMT>
+template <int TT, int NW, bool STORE_S, int FMT, int EPI = kEpiNone>
 hipError_t launch_t(const void* q8, const void* w_rep, void* out, int64_t M, int64_t N,
                     int64_t K, int64_t gm, int64_t gn, int64_t splits, int64_t tm0, int64_t tn0,
-                    int64_t i0, int64_t i1, int64_t j0, int64_t j1, hipStream_t s) {
+                    int64_t i0, int64_t i1, int64_t j0, int64_t j1, hipStream_t s,
+                    const Epilogue& epi = Epilogue{}) {
   constexpr TileShape ts{TT, NW};
   constexpr int64_t lds = ts.lds_bytes(FMT);
   const uint8_t* base = static_cast<const uint8_t*>(q8);
   const int8_t* qs = reinterpret_cast<const int8_t*>(base);
   const float* da_plane = reinterpret_cast<const float*>(base + q8_planes_offset(M, K));
   const uint16_t* tpieces = reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(M, K));
-  auto kern = mmq_kernel<TT, NW, STORE_S, FMT>;
+  auto kern = mmq_kernel<TT, NW, STORE_S, FMT, EPI>;
   // bytes of one token tile (its rows of the q8 buffer) and of one weight-tile group (its
   // records) per super-block column, for the XCD blocks
   const double tok_tile = (double)ts.block_m() * (K / 256) * 400.0;
@@ -520,16 +569,18 @@ hipError_t launch_t(const void* q8, const void* w_rep, void* out, int64_t M, int
                      (size_t)lds, s, qs, da_plane, tpieces,
                      static_cast<const uint8_t*>(w_rep), out, (int)M, (int)N, (int)K, (int)gm,
                      (int)(gm * gn), (int)splits, (int)tm0, (int)tn0, (int)i0, (int)i1, (int)j0,
-                     (int)j1, xb.bm, xb.xgm);
+                     (int)j1, xb.bm, xb.xgm, epi_param<EPI>(epi));
   return hipGetLastError();
 }
 
 // C = the sum of the partial planes ws[0..splits), added in increasing split order (so the
-// result is deterministic), four consecutive elements per thread when N % 4 == 0.
-template <bool VEC4>
+// result is deterministic), four consecutive elements per thread when N % 4 == 0, then the
+// epilogue.
+template <bool VEC4, int EPI>
 __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restrict__ ws,
                                                             float* __restrict__ C, int64_t n,
-                                                            int splits) {
+                                                            int splits, int N,
+                                                            EpiParam<EPI> epi) {
   const int64_t plane = n;
   if constexpr (VEC4) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -539,14 +590,34 @@ __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restr
       const float4 b = *reinterpret_cast<const float4*>(ws + sp * plane + i);
       a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
-    *reinterpret_cast<float4*>(C + i) = a;
+    const int j = EPI == kEpiNone ? 0 : (int)(i % N);
+    *reinterpret_cast<float4*>(C + i) = epi_four<EPI>(epi, a, (size_t)i, j);
   } else {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     float a = ws[i];
     for (int sp = 1; sp < splits; ++sp) a += ws[sp * plane + i];
-    C[i] = a;
+    const int j = EPI == kEpiNone ? 0 : (int)(i % N);
+    C[i] = epi_one<EPI>(epi, a, (size_t)i, j);
   }
+}
+
+// The gated form: planes [splits][M][N] of packed columns, H[M][F] out, one element per
+// work-item (its gate column and, 8 further, its up column).
+__global__ __launch_bounds__(256) void reduce_gated_kernel(const float* __restrict__ ws,
+                                                           float* __restrict__ H, int64_t M, int N,
+                                                           int splits, EpiParam<kEpiGated> epi) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= M * epi.F) return;
+  const int64_t i = n / epi.F;
+  const int f = (int)(n - i * epi.F);
+  const int64_t plane = M * N, at = i * N + 16 * (f >> 3) + (f & 7);
+  float g = ws[at], u = ws[at + 8];
+  for (int sp = 1; sp < splits; ++sp) {
+    g += ws[sp * plane + at];
+    u += ws[sp * plane + at + 8];
+  }
+  H[n] = activate(g, epi.act) * u;
 }
 
 template <int FMT>
@@ -579,7 +650,37 @@ hipError_t launch_fmt(int tile, const void* q8, const void* w_rep, void* out, in
                                                     tn0, i0, i1, j0, j1, s);
 }
 
+template <int EPI>
+hipError_t launch_epi(int tile, const void* q8, const void* w_rep, void* out, int64_t M, int64_t N,
+                      int64_t K, int64_t gm, int64_t gn, const Epilogue& epi, hipStream_t s) {
+  constexpr TileShape L = kLarge, S = kSmall, D = kMedium, H = kHalf;
+  auto go = [&](auto launch) {
+    return launch(q8, w_rep, out, M, N, K, gm, gn, 1, 0, 0, 0, 0, 0, 0, s, epi);
+  };
+  if (tile == 1) return go(launch_t<L.tt, L.nw, false, kFmtQ4K, EPI>);
+  if (tile == 6) return go(launch_t<H.tt, H.nw, false, kFmtQ4K, EPI>);
+  if (tile == 5) return go(launch_t<D.tt, D.nw, false, kFmtQ4K, EPI>);
+  return go(launch_t<S.tt, S.nw, false, kFmtQ4K, EPI>);
+}
+
+template <bool VEC4, int EPI>
+hipError_t launch_reduce(const float* ws, float* C, int64_t M, int64_t N, int64_t splits,
+                         const Epilogue& epi, hipStream_t s) {
+  const int64_t n = M * N, items = VEC4 ? n / 4 : n;
+  hipLaunchKernelGGL((reduce_splits_kernel<VEC4, EPI>), dim3((unsigned)((items + 255) / 256)),
+                     dim3(256), 0, s, ws, C, n, (int)splits, (int)N, epi_param<EPI>(epi));
+  return hipGetLastError();
+}
+
 }  // namespace
+
+hipError_t launch_mmq_epilogue(int tile, const void* q8, const void* w_rep, float* out, int64_t M,
+                               int64_t N, int64_t K, int64_t gm, int64_t gn, const Epilogue& epi,
+                               hipStream_t s) {
+  return epi.kind == kEpiGated
+             ? launch_epi<kEpiGated>(tile, q8, w_rep, out, M, N, K, gm, gn, epi, s)
+             : launch_epi<kEpiAct>(tile, q8, w_rep, out, M, N, K, gm, gn, epi, s);
+}
 
 hipError_t launch_mmq(int tile, const void* q8, const void* w_rep, void* out, int64_t M,
                       int64_t N, int64_t K, int64_t gm, int64_t gn, int64_t splits, int64_t tm0,
@@ -593,18 +694,17 @@ hipError_t launch_mmq(int tile, const void* q8, const void* w_rep, void* out, in
 }
 
 hipError_t launch_reduce_splits(const float* ws, float* C, int64_t M, int64_t N, int64_t splits,
-                                hipStream_t s) {
-  const int64_t n = M * N;
-  if (N % 4 == 0) {
-    const int64_t blocks = (n / 4 + 255) / 256;
-    hipLaunchKernelGGL(reduce_splits_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, ws, C,
-                       n, (int)splits);
-  } else {
-    const int64_t blocks = (n + 255) / 256;
-    hipLaunchKernelGGL(reduce_splits_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, ws,
-                       C, n, (int)splits);
+                                hipStream_t s, const Epilogue& epi) {
+  if (epi.kind == kEpiGated) {
+    hipLaunchKernelGGL(reduce_gated_kernel, dim3((unsigned)((M * epi.F + 255) / 256)), dim3(256),
+                       0, s, ws, C, M, (int)N, (int)splits, epi_param<kEpiGated>(epi));
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  if (epi.kind == kEpiAct)
+    return N % 4 == 0 ? launch_reduce<true, kEpiAct>(ws, C, M, N, splits, epi, s)
+                      : launch_reduce<false, kEpiAct>(ws, C, M, N, splits, epi, s);
+  return N % 4 == 0 ? launch_reduce<true, kEpiNone>(ws, C, M, N, splits, epi, s)
+                    : launch_reduce<false, kEpiNone>(ws, C, M, N, splits, epi, s);
 }
 
 }  // namespace mmq

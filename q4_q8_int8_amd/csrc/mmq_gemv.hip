@@ -44,6 +44,7 @@
 // the order of their terms, so the region holds exactly the bytes and (da, sa) the unfused
 // kernel stages: C is bit for bit that of quantize_q8_1 followed by the unfused kernel, from
 // one launch.
+#include "epilogue.h"
 #include "mmq_device.h"
 #include "quant_device.h"
 
@@ -62,11 +63,12 @@ constexpr int kGemvKS = kGemvSlices * (kGemvWaves / 2);  // K-slices per workgro
 // loaded; without the second stage's registers (79-80 VGPRs for 1-2 tokens, fused 1) three
 // workgroups share a compute unit, which matters most when the grid has more than two per
 // unit (N > 8192 rows).
-template <int MT, bool FUSED, bool ONE>
+template <int MT, bool FUSED, bool ONE, int EPI>
 __global__ __launch_bounds__(kGemvWaves * 64, ONE ? 6 : 1) void mmq_gemv_kernel(
     const int8_t* __restrict__ qs, const uint32_t* __restrict__ words,
     const float* __restrict__ da_plane, const float4* __restrict__ x,
-    const uint8_t* __restrict__ wrep, float* __restrict__ C, int M, int N, int K, int groups) {
+    const uint8_t* __restrict__ wrep, float* __restrict__ C, int M, int N, int K, int groups,
+    EpiParam<EPI> epi) {
   // Wavefronts 0-3 take blocks 0-3 of their slices' super-blocks, wavefronts 4-7 blocks 4-7.
   // Per wavefront and slice: its half of the token bytes [MT][128], then (da, float(sa))
   // [MT][4]; 16 bytes of padding per slice. After the loop the same memory holds the partial
@@ -285,14 +287,31 @@ __global__ __launch_bounds__(kGemvWaves * 64, ONE ? 6 : 1) void mmq_gemv_kernel(
 #pragma unroll
   for (int m = 0; m < MT; ++m) red[((ks * 2 + hf) * MT + m) * kGemvRows + jj] = acc[m];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * kGemvRows; e += kGemvWaves * 64) {
-    const int m = e / kGemvRows, r = e % kGemvRows;
-    const int n = rb * kGemvRows + r;
-    if (m < mc && n < N) {
-      float v = 0.0f;
+  if constexpr (EPI == kEpiGated) {
+    // rows r (gate) and r + 8 (up) of the block: column 8 rb + r of H
+    for (int e = threadIdx.x; e < MT * 8; e += kGemvWaves * 64) {
+      const int m = e >> 3, r = e & 7;
+      const int f = rb * 8 + r;
+      if (m < mc && f < epi.F) {
+        float g = 0.0f, v = 0.0f;
 #pragma unroll
-      for (int k2 = 0; k2 < 2 * kGemvKS; ++k2) v += red[(k2 * MT + m) * kGemvRows + r];
-      C[(size_t)(m0 + m) * N + n] = v;
+        for (int k2 = 0; k2 < 2 * kGemvKS; ++k2) {
+          g += red[(k2 * MT + m) * kGemvRows + r];
+          v += red[(k2 * MT + m) * kGemvRows + r + 8];
+        }
+        C[(size_t)(m0 + m) * epi.F + f] = activate(g, epi.act) * v;
+      }
+    }
+  } else {
+    for (int e = threadIdx.x; e < MT * kGemvRows; e += kGemvWaves * 64) {
+      const int m = e / kGemvRows, r = e % kGemvRows;
+      const int n = rb * kGemvRows + r;
+      if (m < mc && n < N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k2 = 0; k2 < 2 * kGemvKS; ++k2) v += red[(k2 * MT + m) * kGemvRows + r];
+        C[(size_t)(m0 + m) * N + n] = epi_one<EPI>(epi, v, (size_t)(m0 + m) * N + n, n);
+      }
     }
   }
 }
@@ -324,11 +343,11 @@ __global__ __launch_bounds__(kGemvWaves * 64, ONE ? 6 : 1) void mmq_gemv_kernel(
 // accumulator. The NW wavefronts' partial sums are added in wavefront order through LDS.
 // Operand layout of both instructions: A row l % 16 and B column l % 16 take the 8 k values
 // 8 (l / 16) .. + 7; the result of row 4 (l / 16) + r, column l % 16 is register r of lane l.
-template <int NW, int RT>
+template <int NW, int RT, int EPI>
 __global__ __launch_bounds__(64 * NW) void mmq_gemv_mfma_kernel(
     const int8_t* __restrict__ qs, const float* __restrict__ da_plane,
     const uint16_t* __restrict__ tpieces, const uint8_t* __restrict__ wrep,
-    float* __restrict__ C, int M, int N, int K) {
+    float* __restrict__ C, int M, int N, int K, EpiParam<EPI> epi) {
   static_assert(NW >= 4, "the final sum takes 256 work-items");
   static_assert(RT == 1 || RT == 2, "one or two 16-row halves of a tile per workgroup");
   constexpr int kRows = RT * 16;  // weight rows per workgroup
@@ -517,41 +536,60 @@ __global__ __launch_bounds__(64 * NW) void mmq_gemv_mfma_kernel(
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[wave][c16][h * 16 + 4 * kg + r] = acc[h][r];
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * kRows; e += 64 * NW) {
-    const int t = e / kRows, rr = e % kRows;
-    const int n = rb * kRows + rr;
-    if (t < M && n < N) {
-      float v = 0.0f;
+  if constexpr (EPI == kEpiGated) {
+    // packed rows 16 c + r (gate) and 16 c + 8 + r (up): column 8 c + r of the block's H columns
+    for (int e = threadIdx.x; e < 16 * (kRows / 2); e += 64 * NW) {
+      const int t = e / (kRows / 2), fl = e % (kRows / 2);
+      const int f = rb * (kRows / 2) + fl, g = 16 * (fl >> 3) + (fl & 7);
+      if (t < M && f < epi.F) {
+        float a = 0.0f, v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += red[w][t][rr];
-      C[(size_t)t * N + n] = v;
+        for (int w = 0; w < NW; ++w) {
+          a += red[w][t][g];
+          v += red[w][t][g + 8];
+        }
+        C[(size_t)t * epi.F + f] = activate(a, epi.act) * v;
+      }
+    }
+  } else {
+    for (int e = threadIdx.x; e < 16 * kRows; e += 64 * NW) {
+      const int t = e / kRows, rr = e % kRows;
+      const int n = rb * kRows + rr;
+      if (t < M && n < N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) v += red[w][t][rr];
+        C[(size_t)t * N + n] = epi_one<EPI>(epi, v, (size_t)t * N + n, n);
+      }
     }
   }
 }
 
-template <int MT, bool ONE>
+template <int MT, bool ONE, int EPI>
 hipError_t launch_mt(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N, int64_t K,
-                     hipStream_t s) {
+                     hipStream_t s, const Epilogue& epi) {
   const uint8_t* base = static_cast<const uint8_t*>(q8);
   const int64_t groups = (M + MT - 1) / MT;
-  hipLaunchKernelGGL((mmq_gemv_kernel<MT, false, ONE>),
+  hipLaunchKernelGGL((mmq_gemv_kernel<MT, false, ONE, EPI>),
                      dim3((unsigned)((N + kGemvRows - 1) / kGemvRows * groups)),
                      dim3(kGemvWaves * 64), 0, s, reinterpret_cast<const int8_t*>(base),
                      reinterpret_cast<const uint32_t*>(base + M * K),
                      reinterpret_cast<const float*>(base + q8_planes_offset(M, K)), nullptr,
-                     static_cast<const uint8_t*>(w_rep), C, (int)M, (int)N, (int)K, (int)groups);
+                     static_cast<const uint8_t*>(w_rep), C, (int)M, (int)N, (int)K, (int)groups,
+                     epi_param<EPI>(epi));
   return hipGetLastError();
 }
 
-template <int MT, bool ONE>
+template <int MT, bool ONE, int EPI>
 hipError_t launch_fused_mt(const float* x, const void* w_rep, float* C, int64_t M, int64_t N,
-                           int64_t K, hipStream_t s) {
+                           int64_t K, hipStream_t s, const Epilogue& epi) {
   const int64_t groups = (M + MT - 1) / MT;
-  hipLaunchKernelGGL((mmq_gemv_kernel<MT, true, ONE>),
+  hipLaunchKernelGGL((mmq_gemv_kernel<MT, true, ONE, EPI>),
                      dim3((unsigned)((N + kGemvRows - 1) / kGemvRows * groups)),
                      dim3(kGemvWaves * 64), 0, s, nullptr, nullptr, nullptr,
                      reinterpret_cast<const float4*>(x), static_cast<const uint8_t*>(w_rep), C,
-                     (int)M, (int)N, (int)K, (int)groups);
+                     (int)M, (int)N, (int)K, (int)groups,
+                     epi_param<EPI>(epi));
   return hipGetLastError();
 }
 
@@ -590,55 +628,81 @@ int64_t gemv_grid(int64_t M, int64_t N, int mfma_waves, int rows) {
 }
 
 namespace {
-template <int NW, int RT>
+template <int NW, int RT, int EPI>
 hipError_t launch_mfma(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
-                       int64_t K, hipStream_t s) {
+                       int64_t K, hipStream_t s, const Epilogue& epi) {
   const uint8_t* base = static_cast<const uint8_t*>(q8);
   const int64_t lds = gemv_lds_bytes(M, NW, RT * 16);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(mmq_gemv_mfma_kernel<NW, RT>),
+  auto kern = mmq_gemv_mfma_kernel<NW, RT, EPI>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((mmq_gemv_mfma_kernel<NW, RT>), dim3((unsigned)gemv_grid(M, N, NW, RT * 16)),
-                     dim3(64 * NW), (size_t)lds, s, reinterpret_cast<const int8_t*>(base),
+  hipLaunchKernelGGL(kern, dim3((unsigned)gemv_grid(M, N, NW, RT * 16)), dim3(64 * NW),
+                     (size_t)lds, s, reinterpret_cast<const int8_t*>(base),
                      reinterpret_cast<const float*>(base + q8_planes_offset(M, K)),
                      reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(M, K)),
-                     static_cast<const uint8_t*>(w_rep), C, (int)M, (int)N, (int)K);
+                     static_cast<const uint8_t*>(w_rep), C, (int)M, (int)N, (int)K,
+                     epi_param<EPI>(epi));
   return hipGetLastError();
 }
-}  // namespace
 
-hipError_t launch_mmq_gemv(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
-                           int64_t K, int mfma_waves, int rows, hipStream_t s) {
-  if (M < 1 || M > kGemvMaxM || (!mfma_waves && M > kGemvDotMaxM)) return hipErrorInvalidValue;
+template <int EPI>
+hipError_t launch_gemv_epi(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
+                           int64_t K, int mfma_waves, int rows, hipStream_t s,
+                           const Epilogue& epi) {
   if (mfma_waves) {  // the shapes the guard takes (gemv_mfma_waves, gemv_mfma_rows)
-    if (rows == 16 && mfma_waves == 16) return launch_mfma<16, 1>(q8, w_rep, C, M, N, K, s);
-    if (rows == 32 && mfma_waves == 8) return launch_mfma<8, 2>(q8, w_rep, C, M, N, K, s);
-    if (rows == 16 && mfma_waves == 4) return launch_mfma<4, 1>(q8, w_rep, C, M, N, K, s);
+    if (rows == 16 && mfma_waves == 16) return launch_mfma<16, 1, EPI>(q8, w_rep, C, M, N, K, s, epi);
+    if (rows == 32 && mfma_waves == 8) return launch_mfma<8, 2, EPI>(q8, w_rep, C, M, N, K, s, epi);
+    if (rows == 16 && mfma_waves == 4) return launch_mfma<4, 1, EPI>(q8, w_rep, C, M, N, K, s, epi);
     return hipErrorInvalidValue;
   }
   // one step per slice: the single-stage form for 1 and 2 tokens (at 4 and 8 tokens it would
   // spill)
   const bool one = K / 256 <= kGemvKS;
   switch (gemv_dot_group(M)) {
-    case 1: return one ? launch_mt<1, true>(q8, w_rep, C, M, N, K, s)
-                       : launch_mt<1, false>(q8, w_rep, C, M, N, K, s);
-    case 2: return one ? launch_mt<2, true>(q8, w_rep, C, M, N, K, s)
-                       : launch_mt<2, false>(q8, w_rep, C, M, N, K, s);
-    case 4: return launch_mt<4, false>(q8, w_rep, C, M, N, K, s);
-    default: return launch_mt<8, false>(q8, w_rep, C, M, N, K, s);
+    case 1: return one ? launch_mt<1, true, EPI>(q8, w_rep, C, M, N, K, s, epi)
+                       : launch_mt<1, false, EPI>(q8, w_rep, C, M, N, K, s, epi);
+    case 2: return one ? launch_mt<2, true, EPI>(q8, w_rep, C, M, N, K, s, epi)
+                       : launch_mt<2, false, EPI>(q8, w_rep, C, M, N, K, s, epi);
+    case 4: return launch_mt<4, false, EPI>(q8, w_rep, C, M, N, K, s, epi);
+    default: return launch_mt<8, false, EPI>(q8, w_rep, C, M, N, K, s, epi);
+  }
+}
+
+template <int EPI>
+hipError_t launch_gemv_fused_epi(const float* x, const void* w_rep, float* C, int64_t M,
+                                 int64_t N, int64_t K, hipStream_t s, const Epilogue& epi) {
+  // the single-stage form for one token (80 VGPRs; at two tokens it would spill)
+  switch (gemv_dot_group(M)) {
+    case 1: return K / 256 <= kGemvKS ? launch_fused_mt<1, true, EPI>(x, w_rep, C, M, N, K, s, epi)
+                                      : launch_fused_mt<1, false, EPI>(x, w_rep, C, M, N, K, s, epi);
+    case 2: return launch_fused_mt<2, false, EPI>(x, w_rep, C, M, N, K, s, epi);
+    case 4: return launch_fused_mt<4, false, EPI>(x, w_rep, C, M, N, K, s, epi);
+    default: return launch_fused_mt<8, false, EPI>(x, w_rep, C, M, N, K, s, epi);
+  }
+}
+}  // namespace
+
+hipError_t launch_mmq_gemv(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
+                           int64_t K, int mfma_waves, int rows, hipStream_t s,
+                           const Epilogue& epi) {
+  if (M < 1 || M > kGemvMaxM || (!mfma_waves && M > kGemvDotMaxM)) return hipErrorInvalidValue;
+  switch (epi.kind) {
+    case kEpiAct:
+      return launch_gemv_epi<kEpiAct>(q8, w_rep, C, M, N, K, mfma_waves, rows, s, epi);
+    case kEpiGated:
+      return launch_gemv_epi<kEpiGated>(q8, w_rep, C, M, N, K, mfma_waves, rows, s, epi);
+    default: return launch_gemv_epi<kEpiNone>(q8, w_rep, C, M, N, K, mfma_waves, rows, s, epi);
   }
 }
 
 hipError_t launch_mmq_gemv_fused(const float* x, const void* w_rep, float* C, int64_t M,
-                                 int64_t N, int64_t K, hipStream_t s) {
+                                 int64_t N, int64_t K, hipStream_t s, const Epilogue& epi) {
   if (M < 1 || M > kGemvFusedMaxM) return hipErrorInvalidValue;
-  // the single-stage form for one token (80 VGPRs; at two tokens it would spill)
-  switch (gemv_dot_group(M)) {
-    case 1: return K / 256 <= kGemvKS ? launch_fused_mt<1, true>(x, w_rep, C, M, N, K, s)
-                                      : launch_fused_mt<1, false>(x, w_rep, C, M, N, K, s);
-    case 2: return launch_fused_mt<2, false>(x, w_rep, C, M, N, K, s);
-    case 4: return launch_fused_mt<4, false>(x, w_rep, C, M, N, K, s);
-    default: return launch_fused_mt<8, false>(x, w_rep, C, M, N, K, s);
+  switch (epi.kind) {
+    case kEpiAct: return launch_gemv_fused_epi<kEpiAct>(x, w_rep, C, M, N, K, s, epi);
+    case kEpiGated: return launch_gemv_fused_epi<kEpiGated>(x, w_rep, C, M, N, K, s, epi);
+    default: return launch_gemv_fused_epi<kEpiNone>(x, w_rep, C, M, N, K, s, epi);
   }
 }
 

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.h"
+
 namespace mmq {
 
 // Bias word fed to the integer MFMA as its accumulator input: the bit pattern of the float
@@ -134,11 +136,12 @@ int64_t skinny_lds_bytes();
 // compute_units: the device's, which picks the kernel's form (more workgroups than compute
 // units: the form that fits two workgroups per compute unit)
 hipError_t launch_mmq_skinny(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
-                             int64_t K, int64_t compute_units, hipStream_t s);
+                             int64_t K, int64_t compute_units, hipStream_t s,
+                             const Epilogue& epi = Epilogue{});
 // The same kernel quantizing its own f32 activations (few tokens; per-wavefront LDS tile).
 int64_t fused_lds_bytes();
 hipError_t launch_mmq_fused(const float* x, const void* w_rep, float* C, int64_t M, int64_t N,
-                            int64_t K, hipStream_t s);
+                            int64_t K, hipStream_t s, const Epilogue& epi = Epilogue{});
 
 // Product for a handful of tokens (decode), M <= kGemvMaxM, 16 weight rows per workgroup, in
 // two forms. The vector-ALU form (kGemvWaves wavefronts, up to 8 tokens): integer dot
@@ -174,13 +177,18 @@ int64_t gemv_group(int64_t M, int mfma_waves);  // tokens per workgroup
 int64_t gemv_lds_bytes(int64_t M, int mfma_waves, int rows);
 int64_t gemv_grid(int64_t M, int64_t N, int mfma_waves, int rows);
 hipError_t launch_mmq_gemv(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
-                           int64_t K, int mfma_waves, int rows, hipStream_t s);
+                           int64_t K, int mfma_waves, int rows, hipStream_t s,
+                           const Epilogue& epi = Epilogue{});
 // The same kernel quantizing its own f32 activations (same LDS, grid and threads).
 hipError_t launch_mmq_gemv_fused(const float* x, const void* w_rep, float* C, int64_t M,
-                                 int64_t N, int64_t K, hipStream_t s);
+                                 int64_t N, int64_t K, hipStream_t s,
+                                 const Epilogue& epi = Epilogue{});
 
 hipError_t launch_quantize_q8_1(const float* x, int64_t M, int64_t K, void* q8, hipStream_t s);
 hipError_t launch_repack_q4_K(const void* w, int64_t N, int64_t K, void* w_rep, hipStream_t s);
+// Two q4_K matrices of F rows as one packed matrix of pair_rows(F) rows (epilogue.h).
+hipError_t launch_repack_q4_K_pair(const void* w_gate, const void* w_up, int64_t F, int64_t K,
+                                   void* w_pair, hipStream_t s);
 hipError_t launch_repack_q6_K(const void* w, int64_t N, int64_t K, void* w_rep, hipStream_t s);
 
 // GEMM launch: a 1-D grid of gm*gn*splits workgroups covering token tiles [tm0, tm0+gm),
@@ -194,7 +202,11 @@ hipError_t launch_mmq(int tile, const void* q8, const void* w_rep, void* out, in
                       int64_t tn0, bool store_s, int64_t i0, int64_t i1, int64_t j0, int64_t j1,
                       hipStream_t s, int fmt = kFmtQ4K);
 hipError_t launch_reduce_splits(const float* ws, float* C, int64_t M, int64_t N, int64_t splits,
-                                hipStream_t s);
+                                hipStream_t s, const Epilogue& epi = Epilogue{});
+// The q4_K product, unsplit, with an epilogue other than kEpiNone (kEpiGated: N packed rows).
+hipError_t launch_mmq_epilogue(int tile, const void* q8, const void* w_rep, float* out, int64_t M,
+                               int64_t N, int64_t K, int64_t gm, int64_t gn, const Epilogue& epi,
+                               hipStream_t s);
 
 // Host-side helpers of the C ABI (api.cpp) for the other entry-point source: record an error
 // for mmq_last_error, the GEMM entry points' argument checks, and the device check (0 when the
@@ -203,6 +215,8 @@ int api_fail(int status, const char* msg);
 int api_check_gemm_call(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
                         const float* C, const struct mmq_options* opt);
 int api_current_device();
+int api_current_device(int64_t* lds_budget);  // and its per-workgroup LDS limit
+int api_ok();                                 // clears the error text, MMQ_OK
 
 // The f16 comparator path: f32 -> f16 conversion of n values, q4_K -> f16 dequantization,
 // and the f16 GEMM (K % 8 == 0, 2*M*K and 2*N*K below 2^31).

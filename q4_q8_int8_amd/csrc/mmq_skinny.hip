@@ -32,6 +32,7 @@
 // never goes through HBM and the prepass launch disappears, and the result is bit for bit the
 // one of the prepass followed by the unfused kernel: the same bytes, the same arithmetic in
 // the same order.
+#include "epilogue.h"
 #include "mmq_device.h"
 #include "quant_device.h"
 
@@ -54,12 +55,12 @@ constexpr int kRedStride = 65;                     // floats per row of the part
 // compute units. Otherwise (PIPE below) everything a super-block needs is loaded into
 // registers while the previous one is computed, and the MFMA of block b+1 is issued before
 // block b's rescale (238 registers, one workgroup per compute unit).
-template <int KW, bool FUSED, bool LAZY>
+template <int KW, bool FUSED, bool LAZY, int EPI>
 __global__ __launch_bounds__(KW * 64, LAZY ? 4 : 1) void mmq_skinny_kernel(
     const int8_t* __restrict__ qs, const float* __restrict__ da_plane,
     const uint16_t* __restrict__ tpieces, const float4* __restrict__ x,
     const uint8_t* __restrict__ wrep, float* __restrict__ C, int M, int N, int K, int gm,
-    int gmn, int xbm, int xgm) {
+    int gmn, int xbm, int xgm, EpiParam<EPI> epi) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int W_BYTES = kWDsvBytes + kWPieceBytes;
   constexpr int REGION = FUSED ? kFRegion : W_BYTES;
@@ -290,14 +291,33 @@ __global__ __launch_bounds__(KW * 64, LAZY ? 4 : 1) void mmq_skinny_kernel(
   __syncthreads();
   // element e = 32 * token + row of the 32 x 32 tile, so consecutive threads store
   // consecutive output features
-  for (int e = tid; e < 1024; e += KW * 64) {
-    const int il = e >> 5, jl = e & 31;
-    const int r = 4 * (jl >> 3) + (jl & 3), ln = 32 * ((jl >> 2) & 1) + il;
-    float v = 0.0f;
+  if constexpr (EPI == kEpiGated) {
+    // packed rows 16 c + r (gate) and 16 c + 8 + r (up) of the tile: column 8 c + r of H
+    for (int e = tid; e < 512; e += KW * 64) {
+      const int il = e >> 4, fl = e & 15;
+      // row 16 c + r of the tile is register 8 c + r % 4 of lane half (r / 4) % 2; the up row, 8
+      // further, is 4 registers further
+      const int r = 8 * (fl >> 3) + (fl & 3), ln = 32 * ((fl >> 2) & 1) + il;
+      float g = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) v += red[(w * 16 + r) * kRedStride + ln];
-    const int i = m0 + il, j = tn * 32 + jl;
-    if (i < M && j < N) C[(size_t)i * N + j] = v;
+      for (int w = 0; w < KW; ++w) {
+        g += red[(w * 16 + r) * kRedStride + ln];
+        u += red[(w * 16 + r + 4) * kRedStride + ln];
+      }
+      const float v = activate(g, epi.act) * u;
+      const int i = m0 + il, f = tn * 16 + fl;
+      if (i < M && f < epi.F) C[(size_t)i * epi.F + f] = v;
+    }
+  } else {
+    for (int e = tid; e < 1024; e += KW * 64) {
+      const int il = e >> 5, jl = e & 31;
+      const int r = 4 * (jl >> 3) + (jl & 3), ln = 32 * ((jl >> 2) & 1) + il;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) v += red[(w * 16 + r) * kRedStride + ln];
+      const int i = m0 + il, j = tn * 32 + jl;
+      if (i < M && j < N) C[(size_t)i * N + j] = epi_one<EPI>(epi, v, (size_t)i * N + j, j);
+    }
   }
 }
 
@@ -321,26 +341,40 @@ int64_t fused_lds_bytes() {
   return regions > reduce ? regions : reduce;
 }
 
-hipError_t launch_mmq_skinny(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
-                             int64_t K, int64_t compute_units, hipStream_t s) {
+template <int EPI>
+static hipError_t launch_skinny_epi(const void* q8, const void* w_rep, float* C, int64_t M,
+                                    int64_t N, int64_t K, int64_t compute_units, hipStream_t s,
+                                    const Epilogue& epi) {
   const uint8_t* base = static_cast<const uint8_t*>(q8);
   const int8_t* qs = reinterpret_cast<const int8_t*>(base);
   const float* da_plane = reinterpret_cast<const float*>(base + q8_planes_offset(M, K));
   const uint16_t* tpieces = reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(M, K));
   const int64_t gm = (M + 31) / 32, gn = (N + 31) / 32;
   const XcdBlock xb = skinny_xcd_block(gm, gn, K);
-  auto kern = gm * gn > compute_units ? mmq_skinny_kernel<kSkinnyWaves, false, true>
-                                      : mmq_skinny_kernel<kSkinnyWaves, false, false>;
+  auto kern = gm * gn > compute_units ? mmq_skinny_kernel<kSkinnyWaves, false, true, EPI>
+                                      : mmq_skinny_kernel<kSkinnyWaves, false, false, EPI>;
   hipLaunchKernelGGL(kern, dim3((unsigned)(gm * gn)), dim3(kSkinnyWaves * 64),
                      (size_t)skinny_lds_bytes(), s, qs, da_plane, tpieces, nullptr,
                      static_cast<const uint8_t*>(w_rep), C, (int)M, (int)N, (int)K, (int)gm,
-                     (int)(gm * gn), xb.bm, xb.xgm);
+                     (int)(gm * gn), xb.bm, xb.xgm, epi_param<EPI>(epi));
   return hipGetLastError();
 }
 
-hipError_t launch_mmq_fused(const float* x, const void* w_rep, float* C, int64_t M, int64_t N,
-                            int64_t K, hipStream_t s) {
-  auto kern = mmq_skinny_kernel<kSkinnyWaves, true, false>;
+hipError_t launch_mmq_skinny(const void* q8, const void* w_rep, float* C, int64_t M, int64_t N,
+                             int64_t K, int64_t compute_units, hipStream_t s,
+                             const Epilogue& epi) {
+  switch (epi.kind) {
+    case kEpiAct: return launch_skinny_epi<kEpiAct>(q8, w_rep, C, M, N, K, compute_units, s, epi);
+    case kEpiGated:
+      return launch_skinny_epi<kEpiGated>(q8, w_rep, C, M, N, K, compute_units, s, epi);
+    default: return launch_skinny_epi<kEpiNone>(q8, w_rep, C, M, N, K, compute_units, s, epi);
+  }
+}
+
+template <int EPI>
+static hipError_t launch_fused_epi(const float* x, const void* w_rep, float* C, int64_t M,
+                                   int64_t N, int64_t K, hipStream_t s, const Epilogue& epi) {
+  auto kern = mmq_skinny_kernel<kSkinnyWaves, true, false, EPI>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                      hipFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)fused_lds_bytes());
@@ -350,8 +384,18 @@ hipError_t launch_mmq_fused(const float* x, const void* w_rep, float* C, int64_t
   hipLaunchKernelGGL(kern, dim3((unsigned)(gm * gn)), dim3(kSkinnyWaves * 64),
                      (size_t)fused_lds_bytes(), s, nullptr, nullptr, nullptr,
                      reinterpret_cast<const float4*>(x), static_cast<const uint8_t*>(w_rep), C,
-                     (int)M, (int)N, (int)K, (int)gm, (int)(gm * gn), xb.bm, xb.xgm);
+                     (int)M, (int)N, (int)K, (int)gm, (int)(gm * gn), xb.bm, xb.xgm,
+                     epi_param<EPI>(epi));
   return hipGetLastError();
+}
+
+hipError_t launch_mmq_fused(const float* x, const void* w_rep, float* C, int64_t M, int64_t N,
+                            int64_t K, hipStream_t s, const Epilogue& epi) {
+  switch (epi.kind) {
+    case kEpiAct: return launch_fused_epi<kEpiAct>(x, w_rep, C, M, N, K, s, epi);
+    case kEpiGated: return launch_fused_epi<kEpiGated>(x, w_rep, C, M, N, K, s, epi);
+    default: return launch_fused_epi<kEpiNone>(x, w_rep, C, M, N, K, s, epi);
+  }
 }
 
 }  // namespace mmq

@@ -42,6 +42,37 @@ __global__ __launch_bounds__(256) void repack_q4_K_kernel(const uint8_t* __restr
   }
 }
 
+// Two matrices of F rows as the rows of one: packed row 16 b + r is row 8 b + r of the gate for
+// r < 8 and of the up matrix for r >= 8, so the tiles are the 32-row records above with 16 rows
+// of each. Rows past F are zero.
+__global__ __launch_bounds__(256) void repack_q4_K_pair_kernel(const uint8_t* __restrict__ gate,
+                                                               const uint8_t* __restrict__ up,
+                                                               uint8_t* __restrict__ out, int F,
+                                                               int nsb) {
+  const int tile = blockIdx.x / nsb;
+  const int sb = blockIdx.x % nsb;
+  const int tid = threadIdx.x;
+  uint8_t* rec = out + ((size_t)tile * nsb + sb) * kRepTileBytes;
+  auto block_of = [&](int j) -> const uint8_t* {
+    const int f = tile * 16 + 8 * (j >> 4) + (j & 7);
+    if (f >= F) return nullptr;
+    return ((j & 8) ? up : gate) + ((size_t)f * nsb + sb) * 144;
+  };
+  {  // nibbles: 256 chunks of 16 bytes, chunk c = g*64 + h*32 + j
+    const int g = tid >> 6, h = (tid >> 5) & 1, j = tid & 31;
+    const uint8_t* b = block_of(j);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (b) v = *reinterpret_cast<const uint4*>(b + 16 + 32 * g + 16 * h);
+    reinterpret_cast<uint4*>(rec)[tid] = v;
+  }
+  if (tid < kRepTileRows) {
+    const uint8_t* b = block_of(tid);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (b) v = *reinterpret_cast<const uint4*>(b);
+    reinterpret_cast<uint4*>(rec + kRepNibBytes)[tid] = v;
+  }
+}
+
 // q6_K (GGUF layout, 210 bytes per super-block: 128 bytes of low nibbles, 64 bytes of high
 // 2-bit pairs, 16 int8 group scales, f16 d) -> one 10240-byte record per (32-row tile,
 // super-block): the signed values u - 32 as int8 in the GEMM's operand order, then the group
@@ -118,6 +149,16 @@ hipError_t launch_repack_q4_K(const void* w, int64_t N, int64_t K, void* w_rep, 
   hipLaunchKernelGGL(repack_q4_K_kernel, dim3((unsigned)(ntiles * nsb)), dim3(256), 0, s,
                      static_cast<const uint8_t*>(w), static_cast<uint8_t*>(w_rep), (int)N,
                      (int)nsb);
+  return hipGetLastError();
+}
+
+hipError_t launch_repack_q4_K_pair(const void* w_gate, const void* w_up, int64_t F, int64_t K,
+                                   void* w_pair, hipStream_t s) {
+  const int64_t nsb = K / 256;
+  const int64_t ntiles = pair_rows(F) / kRepTileRows;
+  hipLaunchKernelGGL(repack_q4_K_pair_kernel, dim3((unsigned)(ntiles * nsb)), dim3(256), 0, s,
+                     static_cast<const uint8_t*>(w_gate), static_cast<const uint8_t*>(w_up),
+                     static_cast<uint8_t*>(w_pair), (int)F, (int)nsb);
   return hipGetLastError();
 }
 
