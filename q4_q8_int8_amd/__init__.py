@@ -13,6 +13,7 @@ libmmq.so has not been built (python q4_q8_int8_amd/build.py).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -165,7 +166,12 @@ def _dev(t, name: str, nbytes: int, dtype=None) -> int:
     tensor on the current device, of `dtype` when given, holding at least `nbytes` bytes.
     The C ABI takes bare pointers and cannot check buffer sizes itself, so an undersized or
     mistyped buffer is refused here rather than read or written out of bounds."""
-    import torch
+    # the whole check in one expression: a decoding step makes tens of these calls, and the host
+    # side of a call is longer than its kernel (0.4 us here against 0.8 us for the checks below)
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype == dtype)
+            and t.is_contiguous() and t.nbytes >= nbytes
+            and t.get_device() == torch._C._cuda_getDevice()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise MMQArgumentError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if dtype is not None and t.dtype != dtype:
@@ -184,19 +190,16 @@ def _dev(t, name: str, nbytes: int, dtype=None) -> int:
 
 
 def _f32():
-    import torch
     return torch.float32
 
 
 def _i32():
-    import torch
     return torch.int32
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (torch.cuda.current_stream() makes a Stream object: 2.9 us against 0.2)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -209,6 +212,13 @@ def _opts(force_tile: int = MMQ_TILE_AUTO, lds_budget: int = 0, min_workgroups: 
         return None
     return ctypes.byref(mmq_options(force_tile, min_workgroups, lds_budget, workspace,
                                     workspace_bytes, splits, 0))
+
+
+@functools.lru_cache(maxsize=1024)
+def _sized(fn, *args) -> int:
+    """fn(*args) of a size query (host arithmetic on its arguments alone): the wrappers below ask
+    for the same few sizes on every call."""
+    return fn(*args)
 
 
 def _workspace(workspace):
@@ -240,22 +250,22 @@ def mmq_q4K_repacked_bytes(N: int, K: int) -> int:
 
 # ---------------------------------------------------------------- the hot path
 def _gemm_ptrs(M: int, N: int, K: int, q8, w_rep, C):
-    return (_dev(q8, "q8", mmq_q8_1_bytes(M, K)),
-            _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K)),
+    return (_dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K)),
+            _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K)),
             _dev(C, "C", 4 * M * N, _f32()))
 
 
 def quantize_q8_1(x, M: int, K: int, q8, stream=None) -> None:
     """x: f32 [M, K] device tensor; q8: device buffer of mmq_q8_1_bytes(M, K) bytes."""
     xp = _dev(x, "x", 4 * M * K, _f32())
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, K))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
     _check("quantize_q8_1", _lib.quantize_q8_1(xp, M, K, qp, _stream(stream)))
 
 
 def repack_q4_K(w_q4K, N: int, K: int, w_rep, stream=None) -> None:
     """w_q4K: q4_K blocks (mmq_q4K_bytes); w_rep: mmq_q4K_repacked_bytes(N, K) bytes."""
-    wp = _dev(w_q4K, "w_q4K", mmq_q4K_bytes(N, K))
-    rp = _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K))
+    wp = _dev(w_q4K, "w_q4K", _sized(mmq_q4K_bytes, N, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
     _check("repack_q4_K", _lib.repack_q4_K(wp, N, K, rp, _stream(stream)))
 
 
@@ -299,7 +309,7 @@ def mmq_workspace_bytes(M: int, N: int, K: int) -> int:
 def mmq_q4K_f32(M: int, N: int, K: int, x, w_rep, C, stream=None) -> None:
     """Few tokens (M <= 128): C[M, N] from f32 activations x [M, K], quantized in the GEMM."""
     xp = _dev(x, "x", 4 * M * K, _f32())
-    rp = _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
     cp = _dev(C, "C", 4 * M * N, _f32())
     _check("mmq_q4K_f32", _lib.mmq_q4K_f32(M, N, K, xp, rp, cp, _stream(stream)))
 
@@ -308,8 +318,8 @@ def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
                            j1: int, S, stream=None, force_tile: int = MMQ_TILE_AUTO,
                            lds_budget: int = 0) -> None:
     """S: int32 device tensor [K/32, i1-i0, j1-j0] of per-block integer dot products."""
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, K))
-    rp = _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
     sp = _dev(S, "S", 4 * (K // QK8) * max(i1 - i0, 0) * max(j1 - j0, 0), _i32())
     _check("mmq_q4K_q8_1_blockdots",
            _lib.mmq_q4K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp,
@@ -341,7 +351,7 @@ def mmq_q4K_f32_epilogue(M: int, N: int, K: int, x, w_rep, C, bias=None, residua
                          act: int = MMQ_ACT_NONE, stream=None) -> None:
     """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
     xp = _dev(x, "x", 4 * M * K, _f32())
-    rp = _dev(w_rep, "w_rep", mmq_q4K_repacked_bytes(N, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
     cp = _dev(C, "C", 4 * M * N, _f32())
     _check("mmq_q4K_f32_epilogue",
            _lib.mmq_q4K_f32_epilogue(M, N, K, xp, rp, cp, _stream(stream),
@@ -357,9 +367,9 @@ def mmq_q4K_pair_bytes(F: int, K: int) -> int:
 
 def repack_q4_K_pair(w_gate, w_up, F: int, K: int, w_pair, stream=None) -> None:
     """w_gate, w_up: q4_K blocks (mmq_q4K_bytes(F, K)); w_pair: mmq_q4K_pair_bytes(F, K) bytes."""
-    gp = _dev(w_gate, "w_gate", mmq_q4K_bytes(F, K))
-    up = _dev(w_up, "w_up", mmq_q4K_bytes(F, K))
-    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    gp = _dev(w_gate, "w_gate", _sized(mmq_q4K_bytes, F, K))
+    up = _dev(w_up, "w_up", _sized(mmq_q4K_bytes, F, K))
+    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K))
     _check("repack_q4_K_pair", _lib.repack_q4_K_pair(gp, up, F, K, pp, _stream(stream)))
 
 
@@ -375,8 +385,8 @@ def mmq_q4K_q8_1_gated(M: int, F: int, K: int, q8, w_pair, H, act: int = MMQ_ACT
                        stream=None, force_tile: int = MMQ_TILE_AUTO, lds_budget: int = 0,
                        min_workgroups: int = 0, workspace=None, splits: int = 0) -> None:
     """H[M, F] (f32) = act(x Wg^T) * (x Wu^T), q8 (M x K) and a repacked pair (F x K)."""
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, K))
-    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
+    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K))
     hp = _dev(H, "H", 4 * M * F, _f32())
     wp, wb = _workspace(workspace)
     _check("mmq_q4K_q8_1_gated",
@@ -388,7 +398,7 @@ def mmq_q4K_f32_gated(M: int, F: int, K: int, x, w_pair, H, act: int = MMQ_ACT_S
                       stream=None) -> None:
     """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
     xp = _dev(x, "x", 4 * M * K, _f32())
-    pp = _dev(w_pair, "w_pair", mmq_q4K_pair_bytes(F, K))
+    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K))
     hp = _dev(H, "H", 4 * M * F, _f32())
     _check("mmq_q4K_f32_gated",
            _lib.mmq_q4K_f32_gated(M, F, K, xp, pp, hp, _stream(stream), act))
@@ -404,7 +414,7 @@ def mmq_moe_plan_bytes(M: int, E: int, k: int) -> int:
 def mmq_moe_plan(M: int, E: int, k: int, ids, plan, stream=None) -> None:
     """plan (int32, mmq_moe_plan_bytes) from ids int32 [M, k]; an id outside [0, E) is no expert."""
     ip = _dev(ids, "ids", 4 * M * k, _i32())
-    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
     _check("mmq_moe_plan", _lib.mmq_moe_plan(M, E, k, ip, pp, _stream(stream)))
 
 
@@ -415,7 +425,7 @@ def mmq_moe_route(M: int, E: int, k: int, logits, ids, weights, plan=None,
     lp = _dev(logits, "logits", 4 * M * E, _f32())
     ip = _dev(ids, "ids", 4 * M * k, _i32())
     wp = _dev(weights, "weights", 4 * M * k, _f32())
-    pp = None if plan is None else _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    pp = None if plan is None else _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
     _check("mmq_moe_route",
            _lib.mmq_moe_route(M, E, k, lp, score, int(renorm), ip, wp, pp, _stream(stream)))
 
@@ -425,10 +435,10 @@ def mmq_q4K_moe_gated(M: int, E: int, k: int, F: int, D: int, x, plan, w_pairs, 
     """H[M*k, F] (f32): per (token, slot) pair of the plan the gated product of its expert.
     w_pairs: E repacked pairs (mmq_q4K_pair_bytes(F, D) each); q8: scratch, mmq_q8_1_bytes(M, D)."""
     xp = _dev(x, "x", 4 * M * D, _f32())
-    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
-    wp = _dev(w_pairs, "w_pairs", E * mmq_q4K_pair_bytes(F, D))
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
+    wp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D))
     hp = _dev(H, "H", 4 * M * k * F, _f32())
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, D))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, D))
     _check("mmq_q4K_moe_gated",
            _lib.mmq_q4K_moe_gated(M, E, k, F, D, xp, pp, wp, hp, qp, act, _stream(stream)))
 
@@ -439,12 +449,12 @@ def mmq_q4K_moe_down(M: int, E: int, k: int, D: int, F: int, H, plan, weights, w
     w_down: E repacked matrices (mmq_q4K_repacked_bytes(D, F) each); q8: scratch of
     mmq_q8_1_bytes(M*k, F) bytes; residual may be out."""
     hp = _dev(H, "H", 4 * M * k * F, _f32())
-    pp = _dev(plan, "plan", mmq_moe_plan_bytes(M, E, k), _i32())
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
     gp = _dev(weights, "weights", 4 * M * k, _f32())
-    wp = _dev(w_down, "w_down", E * mmq_q4K_repacked_bytes(D, F))
+    wp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F))
     op = _dev(out, "out", 4 * M * D, _f32())
     rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M * k, F))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M * k, F))
     _check("mmq_q4K_moe_down",
            _lib.mmq_q4K_moe_down(M, E, k, D, F, hp, pp, gp, wp, rp, op, qp, _stream(stream)))
 
@@ -463,11 +473,11 @@ def mmq_q4K_moe(M: int, E: int, k: int, D: int, F: int, x, logits, w_pairs, w_do
     router's logits [M, E]. workspace: mmq_moe_workspace_bytes(M, E, k, D, F) bytes."""
     xp = _dev(x, "x", 4 * M * D, _f32())
     lp = _dev(logits, "logits", 4 * M * E, _f32())
-    gp = _dev(w_pairs, "w_pairs", E * mmq_q4K_pair_bytes(F, D))
-    dp = _dev(w_down, "w_down", E * mmq_q4K_repacked_bytes(D, F))
+    gp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D))
+    dp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F))
     op = _dev(out, "out", 4 * M * D, _f32())
     rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
-    sp, sb = _dev(workspace, "workspace", mmq_moe_workspace_bytes(M, E, k, D, F)), \
+    sp, sb = _dev(workspace, "workspace", _sized(mmq_moe_workspace_bytes, M, E, k, D, F)), \
         workspace.numel() * workspace.element_size()
     _check("mmq_q4K_moe",
            _lib.mmq_q4K_moe(M, E, k, D, F, xp, lp, score, int(renorm), gp, act, dp, rp, op, sp, sb,
@@ -489,14 +499,14 @@ def mmq_q6K_repacked_bytes(N: int, K: int) -> int:
 
 def repack_q6_K(w_q6K, N: int, K: int, w_rep, stream=None) -> None:
     """w_q6K: q6_K blocks (mmq_q6K_bytes); w_rep: mmq_q6K_repacked_bytes(N, K) bytes."""
-    wp = _dev(w_q6K, "w_q6K", mmq_q6K_bytes(N, K))
-    rp = _dev(w_rep, "w_rep", mmq_q6K_repacked_bytes(N, K))
+    wp = _dev(w_q6K, "w_q6K", _sized(mmq_q6K_bytes, N, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K))
     _check("repack_q6_K", _lib.repack_q6_K(wp, N, K, rp, _stream(stream)))
 
 
 def _gemm6_ptrs(M: int, N: int, K: int, q8, w_rep, C):
-    return (_dev(q8, "q8", mmq_q8_1_bytes(M, K)),
-            _dev(w_rep, "w_rep", mmq_q6K_repacked_bytes(N, K)),
+    return (_dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K)),
+            _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K)),
             _dev(C, "C", 4 * M * N, _f32()))
 
 
@@ -519,8 +529,8 @@ def mmq_q6K_q8_1_ex(M: int, N: int, K: int, q8, w_rep, C, stream=None,
 def mmq_q6K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, j0: int,
                            j1: int, S, stream=None, force_tile: int = MMQ_TILE_AUTO) -> None:
     """S: int32 device tensor [K/16, i1-i0, j1-j0] of per-group integer dot products."""
-    qp = _dev(q8, "q8", mmq_q8_1_bytes(M, K))
-    rp = _dev(w_rep, "w_rep", mmq_q6K_repacked_bytes(N, K))
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K))
     sp = _dev(S, "S", 4 * (K // 16) * max(i1 - i0, 0) * max(j1 - j0, 0), _i32())
     _check("mmq_q6K_q8_1_blockdots",
            _lib.mmq_q6K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp, _stream(stream),
@@ -548,21 +558,21 @@ def mmq_f16_bytes(rows: int, K: int) -> int:
 def convert_f32_f16(x, M: int, K: int, x_f16, stream=None) -> None:
     """x: f32 [M, K] device tensor; x_f16: device buffer of mmq_f16_bytes(M, K) bytes."""
     xp = _dev(x, "x", 4 * M * K, _f32())
-    hp = _dev(x_f16, "x_f16", mmq_f16_bytes(M, K))
+    hp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
     _check("convert_f32_f16", _lib.convert_f32_f16(xp, M, K, hp, _stream(stream)))
 
 
 def dequantize_q4_K_f16(w_q4K, N: int, K: int, w_f16, stream=None) -> None:
     """w_q4K: q4_K blocks (mmq_q4K_bytes); w_f16: mmq_f16_bytes(N, K) bytes."""
-    wp = _dev(w_q4K, "w_q4K", mmq_q4K_bytes(N, K))
-    hp = _dev(w_f16, "w_f16", mmq_f16_bytes(N, K))
+    wp = _dev(w_q4K, "w_q4K", _sized(mmq_q4K_bytes, N, K))
+    hp = _dev(w_f16, "w_f16", _sized(mmq_f16_bytes, N, K))
     _check("dequantize_q4_K_f16", _lib.dequantize_q4_K_f16(wp, N, K, hp, _stream(stream)))
 
 
 def gemm_f16(M: int, N: int, K: int, x_f16, w_f16, C, stream=None) -> None:
     """C[M, N] (f32 device tensor) = x_f16 [M, K] times w_f16 [N, K]^T, f32 accumulation."""
-    xp = _dev(x_f16, "x_f16", mmq_f16_bytes(M, K))
-    wp = _dev(w_f16, "w_f16", mmq_f16_bytes(N, K))
+    xp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
+    wp = _dev(w_f16, "w_f16", _sized(mmq_f16_bytes, N, K))
     cp = _dev(C, "C", 4 * M * N, _f32())
     _check("gemm_f16", _lib.gemm_f16(M, N, K, xp, wp, cp, _stream(stream)))
 
