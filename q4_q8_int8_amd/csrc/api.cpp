@@ -532,11 +532,13 @@ int api_current_device() {
   DeviceInfo* di;
   return current_device(&di);
 }
-int api_current_device(int64_t* lds_budget) {
+int api_current_device(int64_t* lds_budget, int64_t* compute_units) {
   DeviceInfo* di;
   const int st = current_device(&di);
-  if (!st) *lds_budget = di->lds_budget;
-  return st;
+  if (st) return st;
+  *lds_budget = di->lds_budget;
+  *compute_units = di->compute_units;
+  return MMQ_OK;
 }
 int api_ok() { return ok(); }
 }  // namespace mmq

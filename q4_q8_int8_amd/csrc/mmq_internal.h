@@ -215,7 +215,7 @@ int api_fail(int status, const char* msg);
 int api_check_gemm_call(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
                         const float* C, const struct mmq_options* opt);
 int api_current_device();
-int api_current_device(int64_t* lds_budget);  // and its per-workgroup LDS limit
+int api_current_device(int64_t* lds_budget, int64_t* compute_units);  // and its limits
 int api_ok();                                 // clears the error text, MMQ_OK
 
 // The f16 comparator path: f32 -> f16 conversion of n values, q4_K -> f16 dequantization,

@@ -78,14 +78,16 @@ int hip_status(const char* what, hipError_t e) {
                          : fail(MMQ_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
-// The device, and that the products' kernels fit its LDS.
-int check_device(int64_t M) {
+// The device's compute units, and that the down product's kernel fits its LDS (the gated ones and
+// the router use less than the 64 KiB that every kernel may).
+int check_device(const mmq::MoeShape& m, int64_t* compute_units) {
   int64_t budget = 0;
-  const int st = mmq::api_current_device(&budget);
+  const int st = mmq::api_current_device(&budget, compute_units);
   if (st) return st;
-  if (mmq::moe_lds_bytes(M) > budget)
-    return fail(MMQ_E_LDS, "the experts' products need %lld bytes of LDS, the device allows %lld",
-                (long long)mmq::moe_lds_bytes(M), (long long)budget);
+  const int64_t need = mmq::moe_down_lds_bytes(m, *compute_units);
+  if (need > budget)
+    return fail(MMQ_E_LDS, "the experts' down product needs %lld bytes of LDS, the device allows "
+                           "%lld", (long long)need, (long long)budget);
   return MMQ_OK;
 }
 
@@ -143,15 +145,19 @@ Workspace layout(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F) {
 
 hipError_t run_gated(const mmq::MoeShape& m, const float* x, const int32_t* plan, const void* w,
                      float* H, void* q8, int32_t act, hipStream_t s) {
+  if (mmq::moe_fused(m.M)) return mmq::launch_moe_gated(x, plan, w, H, m, act, s);
   const hipError_t e = mmq::launch_quantize_q8_1(x, m.M, m.D, q8, s);
   return e != hipSuccess ? e : mmq::launch_moe_gated(q8, plan, w, H, m, act, s);
 }
 
 hipError_t run_down(const mmq::MoeShape& m, const float* H, const int32_t* plan,
                     const float* weights, const void* w, const float* residual, float* out,
-                    void* q8, hipStream_t s) {
+                    void* q8, int64_t cus, hipStream_t s) {
+  if (mmq::moe_fused(m.M))
+    return mmq::launch_moe_down(H, plan, weights, w, residual, out, m, cus, s);
   const hipError_t e = mmq::launch_quantize_q8_1(H, m.pairs(), m.F, q8, s);
-  return e != hipSuccess ? e : mmq::launch_moe_down(q8, plan, weights, w, residual, out, m, s);
+  return e != hipSuccess ? e
+                         : mmq::launch_moe_down(q8, plan, weights, w, residual, out, m, cus, s);
 }
 
 }  // namespace
@@ -194,7 +200,7 @@ int mmq_q4K_moe_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, con
                       void* stream) {
   int st = check_gated(M, E, k, F, D, act);
   if (!st) st = check_pointers({x, plan, w_pairs, H, q8});
-  if (!st) st = check_device(M);
+  if (!st) st = mmq::api_current_device();
   if (st) return st;
   return hip_status("mmq_q4K_moe_gated",
                     run_gated(mmq::MoeShape{M, E, k, D, F}, x, plan, w_pairs, H, q8, act,
@@ -205,12 +211,14 @@ int mmq_q4K_moe_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, cons
                      const int32_t* plan, const float* weights, const void* w_down,
                      const float* residual, float* out, void* q8, void* stream) {
   int st = check_down(M, E, k, D, F);
+  const mmq::MoeShape m{M, E, k, D, F};
+  int64_t cus = 0;
   if (!st) st = check_pointers({H, plan, weights, w_down, out, q8}, residual);
-  if (!st) st = check_device(M);
+  if (!st) st = check_device(m, &cus);
   if (st) return st;
   return hip_status("mmq_q4K_moe_down",
-                    run_down(mmq::MoeShape{M, E, k, D, F}, H, plan, weights, w_down, residual, out,
-                             q8, static_cast<hipStream_t>(stream)));
+                    run_down(m, H, plan, weights, w_down, residual, out, q8, cus,
+                             static_cast<hipStream_t>(stream)));
 }
 
 int mmq_moe_workspace_bytes(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F,
@@ -236,18 +244,19 @@ int mmq_q4K_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const flo
   if (workspace_bytes < (size_t)w.total)
     return fail(MMQ_E_ARG, "the layer needs %lld bytes of workspace, %llu given",
                 (long long)w.total, (unsigned long long)workspace_bytes);
-  if ((st = check_device(M))) return st;
+  const mmq::MoeShape m{M, E, k, D, F};
+  int64_t cus = 0;
+  if ((st = check_device(m, &cus))) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* ids = reinterpret_cast<int*>(ws + w.ids);
   float* weights = reinterpret_cast<float*>(ws + w.weights);
   int* plan = reinterpret_cast<int*>(ws + w.plan);
   float* H = reinterpret_cast<float*>(ws + w.H);
-  const mmq::MoeShape m{M, E, k, D, F};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = mmq::launch_moe_route(logits, M, E, k, score, renorm, ids, weights, plan, s);
   if (e == hipSuccess) e = run_gated(m, x, plan, w_pairs, H, ws + w.q8, act, s);
   if (e == hipSuccess)
-    e = run_down(m, H, plan, weights, w_down, residual, out, ws + w.q8, s);
+    e = run_down(m, H, plan, weights, w_down, residual, out, ws + w.q8, cus, s);
   return hip_status("mmq_q4K_moe", e);
 }
 

@@ -39,12 +39,16 @@ hipError_t launch_moe_route(const float* logits, int64_t M, int64_t E, int64_t k
                             int renorm, int* ids, float* weights, int* plan, hipStream_t s);
 hipError_t launch_moe_plan(const int* ids, int64_t M, int64_t E, int64_t k, int* plan,
                            hipStream_t s);
-// H[M*k][F] from the q8 buffer of x (M x D) and E matrices of pair records (F, D).
-hipError_t launch_moe_gated(const void* q8, const int* plan, const void* w, float* H,
+// H[M*k][F] from E matrices of pair records (F, D) and `tokens`: x itself, float32, where the
+// kernel quantizes it (moe_fused), else the q8 buffer of x (M x D).
+hipError_t launch_moe_gated(const void* tokens, const int* plan, const void* w, float* H,
                             const MoeShape& m, int act, hipStream_t s);
-// out[M][D] from the q8 buffer of H (M*k x F) and E matrices of repacked records (D, F).
-hipError_t launch_moe_down(const void* q8, const int* plan, const float* weights, const void* w,
-                           const float* residual, float* out, const MoeShape& m, hipStream_t s);
-int64_t moe_lds_bytes(int64_t M);  // the larger of the two kernels' LDS
+// out[M][D] from E matrices of repacked records (D, F) and `tokens`: H or its q8 buffer (M*k x F).
+hipError_t launch_moe_down(const void* tokens, const int* plan, const float* weights,
+                           const void* w, const float* residual, float* out, const MoeShape& m,
+                           int64_t compute_units, hipStream_t s);
+int64_t moe_down_lds_bytes(const MoeShape& m, int64_t compute_units);
+// Whether the products quantize their own activations: with one token each expert has one column.
+inline bool moe_fused(int64_t M) { return M == 1; }
 
 }  // namespace mmq
