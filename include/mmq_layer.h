@@ -131,7 +131,7 @@ int mmq_moe_plan(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* p
  * A logit of -inf or NaN is never chosen and weighs nothing (a masked expert); a token with fewer
  * than k others gets id -1 and weight 0 in the slots that are left. Where the greatest logit is
  * +inf, the experts that have it share the softmax. plan may be NULL (then any M >= 1, M * E <
- * 2^40, M <= 2^30); otherwise it is written as mmq_moe_plan would, by the same launch.
+ * 2^40, M <= 2^30); otherwise it is written as mmq_moe_plan would.
  * 1 <= E <= 512, 1 <= k <= min(E, 64).
  */
 int mmq_moe_route(int64_t M, int64_t E, int64_t k, const float* logits, int32_t score,

@@ -59,36 +59,44 @@ __global__ __launch_bounds__(64 * NW, kMinWaves<W>) void moe_gated_kernel(
   constexpr int NC = W::kCols, R = W::kRows;
   __shared__ __align__(16) uint8_t smem[NW * W::kLds];
   __shared__ __align__(16) float red[NW][NC][R];
+  __shared__ int pairs[NC];
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int u = (int)(blockIdx.x / (unsigned)blocks), block = (int)(blockIdx.x % (unsigned)blocks);
-  const int P = M * k;
-  const PlanEntry en = plan_entry(plan, u, E, P);
-  if (en.n == 0) return;
-  const int* order = plan + kPlanHead + 4 * entries + en.first;
   const int nsb = K >> 8, nsteps = (nsb + W::SB - 1) / W::SB;
   const int KW = 1 << kw_log2, RB = NW >> kw_log2;
   const int kw = wave & (KW - 1);
   const int tiles = (F + 15) >> 4;
   const int rb = block * RB + (wave >> kw_log2);
   const bool live = rb * R < 32 * tiles && kw < nsteps;
+  const typename W::Tokens tk = W::tokens(tokens, M, K);
+  W w;
+  w.init(smem + wave * W::kLds, lds_addr(smem) + (uint32_t)(wave * W::kLds));
+  typename W::Regs r;
+  // one token: its values do not wait for the plan
+  if constexpr (W::kFused)
+    if (live) w.load_columns(tk, w.group(1, [](int) { return 0u; }), kw, nsb, 0, r);
+
+  const int P = M * k;
+  const PlanEntry en = plan_entry(plan, u, E, P);
+  if (en.n == 0) return;
+  const int* order = plan + kPlanHead + 4 * entries + en.first;
   const int j0 = rb * R & 31;
   const uint8_t* wtile = wrep + ((size_t)en.expert * tiles + (live ? rb * R >> 5 : 0)) *
                                     (size_t)nsb * kRepTileBytes;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(wtile, (uint32_t)nsb * (uint32_t)kRepTileBytes);
-  const typename W::Tokens tk = W::tokens(tokens, M, K);
-  W w;
-  w.init(smem + wave * W::kLds, lds_addr(smem) + (uint32_t)(wave * W::kLds));
 
   for (int g0 = 0; g0 < en.n; g0 += NC) {
-    const typename W::Group g =
-        w.group(en.n - g0 < NC ? en.n - g0 : NC,
-                [&](int m) { return (uint32_t)token_of(pair_at(order, g0 + m, P), km); });
+    const int n = en.n - g0 < NC ? en.n - g0 : NC;
+    if ((int)threadIdx.x < n) pairs[threadIdx.x] = pair_at(order, g0 + (int)threadIdx.x, P);
+    const typename W::Group g = w.group(n, [&](int m) {
+      return W::kFused ? 0u : (uint32_t)token_of(pair_at(order, g0 + m, P), km);
+    });
     typename W::Acc acc;
     w.zero(acc);
     if (live) {
-      typename W::Regs r;
       const typename W::Src first = w.source(rw, j0, nsb, kw, true);
-      w.load(first, nsb, tk, g, r);
+      w.load_weights(first, r);
+      if (!W::kFused || g0 > 0) w.load_columns(tk, g, kw, nsb, 0, r);
       w.finish(tk, g, first, 0, r);
       for (int j = kw, buf = 0; j < nsteps; j += KW, buf ^= 1) {
         const bool more = j + KW < nsteps;
@@ -110,7 +118,7 @@ __global__ __launch_bounds__(64 * NW, kMinWaves<W>) void moe_gated_kernel(
           gs += red[bl * KW + i][m][gr];
           us += red[bl * KW + i][m][gr + 8];
         }
-        H[(size_t)pair_at(order, g0 + m, P) * F + f] = activate(gs, act) * us;
+        H[(size_t)pairs[m] * F + f] = activate(gs, act) * us;
       }
     }
     __syncthreads();
@@ -124,20 +132,21 @@ __global__ __launch_bounds__(64 * NW, kMinWaves<W>) void moe_gated_kernel(
 // product of a pair is finished in one wavefront's registers and goes to LDS once; at the end each
 // output adds its token's slots, in slot order, from there. So the sum over the slots needs no
 // memory, no atomics and no second launch. The plan is copied to LDS first.
-// LDS: [NW] staging, entries, the pairs by position, the positions by pair, then y
-// [part][position][R] of at most `cap` positions in all.
+// LDS: [NW] staging, entries, y [part][position][R] of wpe * P positions, the pairs by position, the
+// positions by pair, the weights.
 template <class W, int NW>
 __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(
     const void* __restrict__ tokens, const int* __restrict__ plan,
     const float* __restrict__ weights, const uint8_t* __restrict__ wrep, const float* residual,
-    float* out, int M, int E, int k, int N, int K, int entries, int cap) {
+    float* out, int M, int E, int k, int N, int K, int entries, int wpe) {
   constexpr int NC = W::kCols, R = W::kRows;
   extern __shared__ __align__(16) uint8_t smem[];
   const int P = M * k;
   int4* ent = reinterpret_cast<int4*>(smem + NW * W::kLds);
   float* y = reinterpret_cast<float*>(ent + entries);
-  int* ord = reinterpret_cast<int*>(y + (size_t)cap * R);
+  int* ord = reinterpret_cast<int*>(y + (size_t)wpe * P * R);
   int* pos = ord + P;
+  float* wts = reinterpret_cast<float*>(pos + P);
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   int used = plan[0];
   if (used < 0 || used > entries) used = 0;
@@ -150,6 +159,7 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(
     const int p = order[i];
     ord[i] = p < 0 || p >= P ? 0 : p;
     pos[i] = -1;
+    wts[i] = weights[i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < P; i += 64 * NW) {  // read after the barrier behind the products
@@ -158,12 +168,16 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(
   }
 
   const int nsb = K >> 8, nsteps = (nsb + W::SB - 1) / W::SB;
-  int wpe = 1;
-  while (2 * wpe * used <= NW && 2 * wpe <= nsteps && 2 * wpe * P <= cap) wpe *= 2;
   const int part = wave & (wpe - 1), stride = NW / wpe;
   const int rb = (int)blockIdx.x;
   const int tiles = (N + 31) >> 5;
   const int tile = rb * R >> 5, j0 = rb * R & 31;
+  // the residual of this work-item's first output, read while the products run
+  float res = 0.0f;
+  {
+    const int t = (int)threadIdx.x / R, n = rb * R + (int)threadIdx.x % R;
+    if (residual && t < M && n < N) res = residual[(size_t)t * N + n];
+  }
   const typename W::Tokens tk = W::tokens(tokens, P, K);
   W w;
   w.init(smem + wave * W::kLds, lds_addr(smem) + (uint32_t)(wave * W::kLds));
@@ -220,7 +234,8 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(
   typename W::Regs r;
   if (a.j >= 0) {
     const typename W::Src first = source(a);
-    w.load(first, nsb, tk, a.g, r);
+    w.load_weights(first, r);
+    w.load_columns(tk, a.g, a.j, nsb, 0, r);
     w.finish(tk, a.g, first, 0, r);
   }
   for (int buf = 0; a.j >= 0; buf ^= 1) {
@@ -248,11 +263,12 @@ __global__ __launch_bounds__(64 * NW, 4) void moe_down_kernel(
         if (i >= 0) {
           float d = y[(size_t)i * R + r];
           for (int q = 1; q < wpe; ++q) d += y[((size_t)q * P + i) * R + r];
-          v = __builtin_fmaf(weights[t * k + s], d, v);
+          v = __builtin_fmaf(wts[t * k + s], d, v);
         }
       }
       const size_t at = (size_t)t * N + n;
-      out[at] = residual ? v + residual[at] : v;
+      if (residual) v += e == (int)threadIdx.x ? res : residual[at];
+      out[at] = v;
     }
   }
 }
@@ -272,12 +288,20 @@ hipError_t launch_gated(const void* tokens, const int* plan, const void* w, floa
   return hipGetLastError();
 }
 
-// Positions of y: the pairs, and up to 512 where an expert's K is split over wavefronts.
-int64_t down_cap(const MoeShape& m) { return m.pairs() > 512 ? m.pairs() : 512; }
+// Parts of an expert's K in the down product: as many as there are wavefronts per entry, steps,
+// and room for (512 positions of y, or the pairs).
+template <class W, int NW>
+int64_t down_parts(const MoeShape& m) {
+  const int64_t nsteps = (m.F / 256 + W::SB - 1) / W::SB;
+  int64_t wpe = 1;
+  while (2 * wpe * m.entries() <= NW && 2 * wpe <= nsteps && 2 * wpe * m.pairs() <= 512) wpe *= 2;
+  return wpe;
+}
 
 template <class W, int NW>
 int64_t down_lds(const MoeShape& m) {
-  return NW * W::kLds + 16 * m.entries() + 8 * m.pairs() + 4 * down_cap(m) * W::kRows;
+  return NW * W::kLds + 16 * m.entries() + 12 * m.pairs() +
+         4 * down_parts<W, NW>(m) * m.pairs() * W::kRows;
 }
 
 template <class W, int NW>
@@ -291,7 +315,7 @@ hipError_t launch_down(const void* tokens, const int* plan, const float* weights
   hipLaunchKernelGGL(kern, dim3((unsigned)((m.D + W::kRows - 1) / W::kRows)), dim3(64 * NW),
                      (size_t)lds, s, tokens, plan, weights, static_cast<const uint8_t*>(w),
                      residual, out, (int)m.M, (int)m.E, (int)m.k, (int)m.D, (int)m.F,
-                     (int)m.entries(), (int)down_cap(m));
+                     (int)m.entries(), (int)down_parts<W, NW>(m));
   return hipGetLastError();
 }
 

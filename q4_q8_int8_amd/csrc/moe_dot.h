@@ -35,6 +35,7 @@ template <int RW, int MT, bool FUSED>
 struct DotWave {
   static constexpr int kRows = RW;
   static constexpr int kCols = MT;
+  static constexpr bool kFused = FUSED;
   static constexpr int SL = 64 / RW;       // slices
   static constexpr int SB = SL / 2;        // super-blocks per step
   static constexpr int kQ = MT * SL * 128;  // LDS: token bytes, then float pairs
@@ -173,13 +174,10 @@ struct DotWave {
       }
     }
   }
-  // All of a first step's loads.
-  __device__ __forceinline__ void load(const Src& f, int nsb, const Tokens& t, const Group& g,
-                                       Regs& r) const {
+  __device__ __forceinline__ void load_weights(const Src& f, Regs& r) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_nib(f, i, r);
     load_hdr(f, r);
-    load_columns(t, g, f.j, nsb, 0, r);
   }
 
   // What is left of a step's staging once its loads may be waited for.

@@ -34,6 +34,7 @@ struct MfmaWave {
   static_assert(KS == 1 || (KS == 2 && RT == 1), "forms");
   static constexpr int kRows = 16 * RT / KS;
   static constexpr int kCols = NT / KS;
+  static constexpr bool kFused = false;
   static constexpr int SB = KS;
   // LDS: per 16 rows the expanded scales (dsv f32 [8][16], the dmv pieces bf16 [3][16][8]), then
   // twice the columns' operands of a super-block: int8 [NT][256], the 16-byte chunk c of column t
@@ -135,13 +136,13 @@ struct MfmaWave {
     for (int h = 0; h < RT; ++h)
       r.hdr[h] = buf_load16(f.rw, f.rec + kRepNibBytes + (f.j0 + h * 16 + row) * 16);
   }
-  __device__ __forceinline__ void load_words(const Tokens& t, const Group& g, const Src& f, int i,
+  __device__ __forceinline__ void load_words(const Tokens& t, const Group& g, int s, bool ok, int i,
                                              Regs& r) const {
-    const uint32_t at = (g.row * t.kb + (uint32_t)(f.s + sel) * 8u) * 4u + 16u * i;
-    r.wd[i] = buf_load16(t.rwd, f.ok ? at : kNoRecord);  // no super-block: scales of 0
+    const uint32_t at = (g.row * t.kb + (uint32_t)(s + sel) * 8u) * 4u + 16u * i;
+    r.wd[i] = buf_load16(t.rwd, ok ? at : kNoRecord);  // no super-block: scales of 0
   }
-  __device__ __forceinline__ void load_columns(const Tokens& t, const Group& g, int s,
-                                               int buf) const {
+  __device__ __forceinline__ void stage_columns(const Tokens& t, const Group& g, int s,
+                                                int buf) const {
     const uint32_t tok = lds_at + RT * kScale + (NBUF == 2 ? buf * kBuf : 0);
 #pragma unroll
     for (int i = 0; i < NT / 4; ++i) {
@@ -156,22 +157,25 @@ struct MfmaWave {
             (((uint32_t)(s + lane % NT / kCols) * 3u + (uint32_t)(lane / NT)) * t.rows + g.prow) *
                 16u);
   }
-  // All of a first step's loads.
-  __device__ __forceinline__ void load(const Src& f, int, const Tokens& t, const Group& g,
-                                       Regs& r) const {
+  __device__ __forceinline__ void load_weights(const Src& f, Regs& r) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_nib(f, i, r);
     load_hdr(f, r);
-    load_words(t, g, f, 0, r);
-    load_words(t, g, f, 1, r);
-    if (NBUF == 2) load_columns(t, g, f.s, 0);
+  }
+  // What of step j's columns is loaded ahead of finish().
+  __device__ __forceinline__ void load_columns(const Tokens& t, const Group& g, int j, int nsb,
+                                               int buf, Regs& r) const {
+    const bool ok = KS == 1 || KS * j + sel < nsb;
+    load_words(t, g, KS * j, ok, 0, r);
+    load_words(t, g, KS * j, ok, 1, r);
+    if (NBUF == 2) stage_columns(t, g, KS * j, buf);
   }
 
   // Once the previous step is computed: wait for the loads and expand the scales, lane (c16, kg)
   // sub-blocks 2 kg and 2 kg + 1 of row c16 of each half.
   __device__ __forceinline__ void finish(const Tokens& t, const Group& g, const Src& f, int,
                                          const Regs& r) const {
-    if (NBUF == 1) load_columns(t, g, f.s, 0);
+    if (NBUF == 1) stage_columns(t, g, f.s, 0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
 #pragma unroll
@@ -206,7 +210,7 @@ struct MfmaWave {
   __device__ __forceinline__ void compute(const Group&, int, int, int buf, Regs& r, Acc& acc,
                                           bool more, const Src& f, const Tokens& t,
                                           const Group& gn) const {
-    if (NBUF == 2 && more) load_columns(t, gn, f.s, buf ^ 1);
+    if (NBUF == 2 && more) stage_columns(t, gn, f.s, buf ^ 1);
     load_hdr(f, r);
     const uint8_t* stok = lds + RT * kScale + (NBUF == 2 ? buf * kBuf : 0);
     // term2 piece pairs of this lane's k-group: (0,0) (0,1) (1,0) (0,2) in the first instruction,
@@ -238,7 +242,7 @@ struct MfmaWave {
       if (b & 1) {
         __builtin_amdgcn_sched_barrier(0);  // not before: the registers are in use
         load_nib(f, b >> 1, r);
-        if ((b & 3) == 3) load_words(t, gn, f, b >> 2, r);
+        if ((b & 3) == 3) load_words(t, gn, f.s, f.ok, b >> 2, r);
       }
     }
     const uint8_t* pc = stok + NT * 256;

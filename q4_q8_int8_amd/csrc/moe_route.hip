@@ -6,9 +6,9 @@
 // past E), so a maximum over the wavefront is six v_max_u32 with lane moves, and k of them, each
 // removing its winner, give the experts in order; among equal logits the lowest expert wins.
 // Everything fits a few thousand cycles, so what bounds the call is its launch and one read of the
-// logits; the plan is therefore made by the same launch when it is asked for: one workgroup then
-// takes all (at most 64) tokens and sorts the pairs by expert from a bit matrix in LDS (expert x
-// pair), whose bits are set with integer atomics (order-free) and counted.
+// logits; the plan is therefore made by the same launch for a few tokens: one workgroup then takes
+// them all and sorts the pairs by expert from a bit matrix in LDS (expert x pair), whose bits are
+// set with integer atomics (order-free) and counted. For more it is a launch of its own (launch_route).
 #include "moe_internal.h"
 
 namespace mmq {
@@ -227,6 +227,14 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int* __restric
 template <int NV>
 hipError_t launch_route(const float* logits, int64_t M, int64_t E, int64_t k, int score, int renorm,
                         int* ids, float* weights, int* plan, hipStream_t s) {
+  // One launch for both while the plan's one workgroup has few tokens per wavefront to route: graph
+  // replays, one launch against two, 4.9 / 6.5 us for 16 tokens of 64 experts, 6.7 / 7.5 for 16 of
+  // 256, but 10.0 / 7.6 for 32 of 256, 10.2 / 6.9 for 64 of 64 and 16.6 / 7.8 for 64 of 256.
+  if (plan && M * (NV + 1) > 96) {
+    const hipError_t e =
+        launch_route<NV>(logits, M, E, k, score, renorm, ids, weights, nullptr, s);
+    return e != hipSuccess ? e : launch_moe_plan(ids, M, E, k, plan, s);
+  }
   if (plan)
     hipLaunchKernelGGL(route_plan_kernel<NV>, dim3(1), dim3(kPlanThreads), 0, s, logits, (int)M,
                        (int)E, (int)k, score, renorm, ids, weights, plan);
