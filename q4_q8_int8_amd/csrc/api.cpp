@@ -152,6 +152,11 @@ constexpr TileCost kTileCosts[] = {{MMQ_TILE_LARGE, 3.4, 1.0},
                                    {MMQ_TILE_MEDIUM, 2.1, 1.0},
                                    {MMQ_TILE_SMALL, 1.7, 2.5}};
 constexpr double kUsPerPartialMB = 0.45;
+// What the second kernel of a split costs beside its traffic, counted for the products with an
+// epilogue (the plain product's choices, and so its bits, stay as they were). Graph replays with
+// bias and gelu, skinny tile against the split that is cheapest without this term: 77 x 1376 x
+// 4096 10.7 against 13.5 us, 20 x 2752 x 4096 9.7 against 12.2.
+constexpr double kUsSecondKernel = 3.0;
 // The skinny kernel in the same model: one workgroup per 32 x 32 output tile, its 8
 // wavefronts each walking K/8 super-blocks; one workgroup per compute unit at a time when
 // the grid fits the device in one round, else the form that shares a compute unit between
@@ -174,7 +179,8 @@ mmq::TileShape tile_shape(int tile) {
 
 // The guard: which tile, given the LDS budget and the compute units the grid should fill.
 int plan(int64_t M, int64_t N, int64_t K, const mmq_options* opt, int64_t budget,
-         int64_t compute_units, mmq_kernel_info* info, int fmt = mmq::kFmtQ4K) {
+         int64_t compute_units, mmq_kernel_info* info, int fmt = mmq::kFmtQ4K,
+         bool epilogue = false) {
   const bool q6 = fmt == mmq::kFmtQ6K;
   memset(info, 0, sizeof(*info));
   if (opt && opt->lds_budget > 0) budget = opt->lds_budget;
@@ -269,6 +275,7 @@ int plan(int64_t M, int64_t N, int64_t K, const mmq_options* opt, int64_t budget
         const double per_wg = (double)((nsb + sp - 1) / sp);
         double cost = c.us_per_sb * rounds * per_wg;
         if (sp > 1) cost += kUsPerPartialMB * (double)(8 * sp + 4) * (double)M * (double)N * 1e-6;
+        if (sp > 1 && epilogue) cost += kUsSecondKernel;
         if (cost < best) { best = cost; best_tile = c.tile; best_sp = sp; }
       }
     }
@@ -387,7 +394,8 @@ int gemm_ex(int fmt, int64_t M, int64_t N, int64_t K, const void* q8, const void
   DeviceInfo* di;
   if ((st = current_device(&di))) return st;
   mmq_kernel_info info;
-  st = plan(M, N, K, opt, di->lds_budget, di->compute_units, &info, fmt);
+  st = plan(M, N, K, opt, di->lds_budget, di->compute_units, &info, fmt,
+            epi.kind != mmq::kEpiNone);
   g_last = info;
   if (st) return st;
   return launch_planned(info, M, N, K, q8, w_rep, C, opt ? opt->workspace : nullptr,
@@ -440,6 +448,21 @@ int gemm_f32(const char* fn, int64_t M, int64_t N, int64_t K, const float* x, co
   hipError_t e = gemv ? mmq::launch_mmq_gemv_fused(x, w_rep, C, M, N, K, s, epi)
                       : mmq::launch_mmq_fused(x, w_rep, C, M, N, K, s, epi);
   if (e != hipSuccess) return fail(MMQ_E_HIP, "%s launch: %s", fn, hipGetErrorString(e));
+  return ok();
+}
+
+// The workspace the guard would use, given an unlimited one.
+int workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes, bool epilogue) {
+  if (!bytes) return fail(MMQ_E_ARG, "bytes is NULL");
+  int st = check_gemm_shape(M, N, K);
+  if (st) return st;
+  mmq_options o = {};
+  o.workspace_bytes = INT64_MAX;
+  mmq_kernel_info info;
+  if ((st = plan(M, N, K, &o, kDefaultLdsBudget, kDefaultComputeUnits, &info, mmq::kFmtQ4K,
+                 epilogue)))
+    return st;
+  *bytes = (size_t)info.workspace_bytes;
   return ok();
 }
 
@@ -624,15 +647,7 @@ int mmq_q4K_q8_1_ex(int64_t M, int64_t N, int64_t K, const void* q8, const void*
 }
 
 int mmq_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
-  if (!bytes) return fail(MMQ_E_ARG, "bytes is NULL");
-  int st = check_gemm_shape(M, N, K);
-  if (st) return st;
-  mmq_options o = {};
-  o.workspace_bytes = INT64_MAX;
-  mmq_kernel_info info;
-  if ((st = plan(M, N, K, &o, kDefaultLdsBudget, kDefaultComputeUnits, &info))) return st;
-  *bytes = (size_t)info.workspace_bytes;
-  return ok();
+  return workspace_bytes(M, N, K, bytes, false);
 }
 
 int mmq_q4K_q8_1(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep, float* C,
@@ -697,7 +712,7 @@ int mmq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t* bytes) {
   if (!bytes) return fail(MMQ_E_ARG, "bytes is NULL");
   mmq::Epilogue e;
   const int st = make_gated(F, MMQ_ACT_NONE, &e);
-  return st ? st : mmq_workspace_bytes(M, mmq::pair_rows(F), K, bytes);
+  return st ? st : workspace_bytes(M, mmq::pair_rows(F), K, bytes, true);
 }
 
 int mmq_q4K_q8_1_gated(int64_t M, int64_t F, int64_t K, const void* q8, const void* w_pair,

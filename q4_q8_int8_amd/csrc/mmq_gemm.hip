@@ -607,17 +607,19 @@ __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restr
 __global__ __launch_bounds__(256) void reduce_gated_kernel(const float* __restrict__ ws,
                                                            float* __restrict__ H, int64_t M, int N,
                                                            int splits, EpiParam<kEpiGated> epi) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= M * epi.F) return;
-  const int64_t i = n / epi.F;
-  const int f = (int)(n - i * epi.F);
-  const int64_t plane = M * N, at = i * N + 16 * (f >> 3) + (f & 7);
-  float g = ws[at], u = ws[at + 8];
-  for (int sp = 1; sp < splits; ++sp) {
-    g += ws[sp * plane + at];
-    u += ws[sp * plane + at + 8];
+  const int64_t plane = M * N;
+  for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < M * epi.F;
+       n += (int64_t)gridDim.x * 256) {
+    const int64_t i = n / epi.F;
+    const int f = (int)(n - i * epi.F);
+    const int64_t at = i * N + 16 * (f >> 3) + (f & 7);
+    float g = ws[at], u = ws[at + 8];
+    for (int sp = 1; sp < splits; ++sp) {
+      g += ws[sp * plane + at];
+      u += ws[sp * plane + at + 8];
+    }
+    H[n] = activate(g, epi.act) * u;
   }
-  H[n] = activate(g, epi.act) * u;
 }
 
 template <int FMT>
@@ -696,8 +698,10 @@ hipError_t launch_mmq(int tile, const void* q8, const void* w_rep, void* out, in
 hipError_t launch_reduce_splits(const float* ws, float* C, int64_t M, int64_t N, int64_t splits,
                                 hipStream_t s, const Epilogue& epi) {
   if (epi.kind == kEpiGated) {
-    hipLaunchKernelGGL(reduce_gated_kernel, dim3((unsigned)((M * epi.F + 255) / 256)), dim3(256),
-                       0, s, ws, C, M, (int)N, (int)splits, epi_param<kEpiGated>(epi));
+    const int64_t blocks = (M * epi.F + 255) / 256, most = (int64_t)1 << 20;
+    hipLaunchKernelGGL(reduce_gated_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                       dim3(256), 0, s, ws, C, M, (int)N, (int)splits,
+                       epi_param<kEpiGated>(epi));
     return hipGetLastError();
   }
   if (epi.kind == kEpiAct)

@@ -106,11 +106,14 @@ int check_route_options(int32_t score, int32_t renorm) {
 
 int check_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, int32_t act) {
   int st = check_routing(M, E, k, true);
-  if (!st) st = check_product("F", F, "D", D, M, kMaxDim / 2);
+  if (!st) st = check_product("F", F, "D", D, M, kMaxDim);
   if (!st) st = check_act(act);
-  // one workgroup per (used expert, 16 columns) on a 1-D grid
-  if (!st && (F + 15) / 16 * mmq::kMoeMaxPairs >= ((int64_t)1 << 31))
-    st = fail(MMQ_E_SHAPE, "F = %lld too large", (long long)F);
+  // at most two workgroups of 256 work-items per (expert, 16 columns), on a 1-D grid of fewer than
+  // 2^32 work-items
+  const int64_t entries = mmq::MoeShape{M, E, k, D, F}.entries();
+  if (!st && (F + 15) / 16 * entries >= ((int64_t)1 << 23))
+    st = fail(MMQ_E_SHAPE, "min(E, M*k) * ceil(F/16) = %lld is not below 2^23",
+              (long long)((F + 15) / 16 * entries));
   return st;
 }
 

@@ -184,6 +184,7 @@ struct DotWave {
   __device__ __forceinline__ void finish(const Tokens&, const Group&, const Src&, int buf,
                                          const Regs& r) const {
     uint8_t* b = lds + buf * kBuf;
+    asm volatile("" ::: "memory");  // the previous step's LDS reads stay above
     if constexpr (FUSED) {
       float a = 0.0f;
 #pragma unroll

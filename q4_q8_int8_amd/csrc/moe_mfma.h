@@ -175,9 +175,15 @@ struct MfmaWave {
   // sub-blocks 2 kg and 2 kg + 1 of row c16 of each half.
   __device__ __forceinline__ void finish(const Tokens& t, const Group& g, const Src& f, int,
                                          const Regs& r) const {
-    if (NBUF == 1) stage_columns(t, g, f.s, 0);
-    asm volatile("" ::: "memory");
+    asm volatile("" ::: "memory");  // the previous step's LDS reads stay above
+    if (NBUF == 1) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): ... and are done before the buffer's loads
+      stage_columns(t, g, f.s, 0);
+      asm volatile("" ::: "memory");
+    }
     __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int h = 0; h < RT; ++h) {
       const uint32_t w0 = (uint32_t)r.hdr[h][0], s0 = (uint32_t)r.hdr[h][1],

@@ -379,7 +379,8 @@ def gpu_down(ex, H, ids, wts, residual=None, out=None):
 
 MOE = [(1, 8, 2, 512, 256), (1, 16, 8, 2048, 512), (2, 4, 4, 256, 768), (3, 8, 3, 768, 40),
        (4, 8, 2, 512, 33), (5, 8, 4, 512, 256), (16, 4, 2, 256, 512), (17, 3, 3, 512, 256),
-       (64, 8, 2, 256, 256), (64, 12, 8, 256, 256)]
+       (64, 8, 2, 256, 256), (64, 12, 8, 256, 256), (3, 16, 2, 2048, 64), (6, 3, 2, 4352, 24),
+       (9, 3, 3, 512, 768)]
 
 
 @pytest.mark.parametrize("M,E,k,D,F", MOE)
@@ -396,7 +397,8 @@ def test_moe_gated(M, E, k, D, F, kind):
 
 
 @pytest.mark.parametrize("M,E,k,D,F", [c for c in MOE if c[4] % 256 == 0]
-                         + [(1, 4, 2, 20, 512), (6, 4, 2, 45, 512)])
+                         + [(1, 4, 2, 20, 512), (6, 4, 2, 45, 512), (1, 3, 2, 2064, 768),
+                            (2, 3, 2, 2064, 256), (12, 3, 2, 2070, 512)])
 @pytest.mark.parametrize("kind", ["distinct", "repeated", "one", "padded", "none"])
 def test_moe_down(M, E, k, D, F, kind):
     ex = ExpertsDown(E, D, F)
@@ -422,6 +424,19 @@ class ExpertsDown:
         self.E, self.D, self.F = E, D, F
         self.down = np.stack([lu.weights(D, F, seed + e) for e in range(E)])
         self.w_out = torch.cat([gpu_repack(self.down[e], D, F) for e in range(E)])
+
+
+def test_many_experts():
+    """The plan's largest sizes: 512 experts, 512 pairs, all different and all the same."""
+    M, E, k, D, F = 64, 512, 8, 256, 256
+    ex = Experts(E, D, F)
+    x = synth.activations("normal", M, D, 8)
+    for ids in (np.arange(512).reshape(M, k).astype(np.int32), np.full((M, k), 511, np.int32)):
+        H = host(gpu_gated(ex, x, ids))
+        lu.assert_close(H, *lu.experts_gated(x, ids, ex.gate, ex.up, "silu"))
+        wts = np.random.default_rng(9).random((M, k)).astype(np.float32)
+        lu.assert_close(host(gpu_down(ex, H, ids, wts)),
+                        *lu.experts_down(H, ids, wts, ex.down, None))
 
 
 def test_moe_gated_one_expert_per_token_is_the_gated_product():

@@ -110,6 +110,20 @@ def test_gated_bad_act(act):
                         None) == mmq.MMQ_E_ARG
 
 
+def test_workspace_of_the_gated_product():
+    """A split's second kernel is counted, so K is split at most where the plain product's is."""
+    for M, F, K in ((77, 688, 4096), (300, 1376, 4096), (20, 1376, 4096), (512, 512, 11008)):
+        assert (mmq.mmq_gated_workspace_bytes(M, F, K)
+                <= mmq.mmq_workspace_bytes(M, 32 * ((F + 15) // 16), K))
+    assert mmq.mmq_gated_workspace_bytes(77, 688, 4096) == 0
+
+
+def test_gated_experts_grid_limit():
+    # 8 experts, ceil(F/16) = 2^20: 2^23 in all
+    a = [4, 8, 2, 1 << 24, 256, P, P, P, P, P, 2, None]
+    assert mmq.raw_call("mmq_q4K_moe_gated", *a) == mmq.MMQ_E_SHAPE
+
+
 def test_epilogue_options_are_checked():
     o = mmq.mmq_options(99, 0, 0, None, 0, 0, 0)
     assert mmq.raw_call(EPI[0], 4, 64, 256, P, P, P, None, _epi(act=1),
