@@ -60,7 +60,9 @@ int mmq_q4K_q8_1_epilogue(int64_t M, int64_t N, int64_t K, const void* q8, const
                           const mmq_options* opt);
 
 /* As mmq_q4K_f32 (few tokens, 1 <= M <= 128, float32 activations quantized in the product, one
- * launch) with the epilogue. It pays up to about 4 tokens, as mmq_q4K_f32 does. */
+ * launch) with the epilogue. Against quantize_q8_1 and the product (graph replays, residual): 1
+ * token 5.0 / 7.1 us at 4096 x 4096, 13.6 / 15.4 at 22016 x 4096; 2 tokens 6.0 / 7.5 and 18.3 / 16.1;
+ * 4 tokens 7.9 / 8.4 and 38 / 20. */
 int mmq_q4K_f32_epilogue(int64_t M, int64_t N, int64_t K, const float* x, const void* w_rep,
                          float* C, void* stream, const mmq_epilogue* epi);
 

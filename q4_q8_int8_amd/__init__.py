@@ -49,9 +49,11 @@ ACTIVATIONS = {"none": MMQ_ACT_NONE, "relu": MMQ_ACT_RELU, "silu": MMQ_ACT_SILU,
 MMQ_SCORE_SOFTMAX, MMQ_SCORE_SIGMOID = range(2)
 SCORES = {"softmax": MMQ_SCORE_SOFTMAX, "sigmoid": MMQ_SCORE_SIGMOID}
 MOE_MAX_TOKENS, MOE_MAX_PAIRS, MOE_MAX_EXPERTS, MOE_MAX_SLOTS = 64, 512, 512, 64
-# up to this many tokens the products from float32 activations (mmq_q4K_f32 and its forms) beat
-# quantize_q8_1 followed by the product
-FUSED_TOKENS = 4
+# up to this many tokens the products from float32 activations (mmq_q4K_f32 and its forms) are the
+# better choice at most sizes: one launch, 1 token 1.5 to 2 us faster than quantize_q8_1 and the
+# product at 4096 to 22016 rows; 2 tokens 6.0 against 7.5 us at 4096 x 4096 and 18.3 against 16.1 at
+# 22016 x 4096; 3 and more only at 4096 x 4096 or below
+FUSED_TOKENS = 2
 
 
 class mmq_options(ctypes.Structure):

@@ -8,11 +8,12 @@
 // workgroup finds the rows of its product, the expert's columns below, in one list.
 //
 // Both are bound by reading the used experts' weights (4.5 bits each; nothing else is of their
-// size) until the vector ALU is: a wavefront's product is a DotWave (moe_dot.h, a few columns) or
-// a MfmaWave (moe_mfma.h, up to 16), chosen on the host from the columns an expert has on average.
-// An expert with more columns than the form takes is worked through in groups, its weights coming
-// from the cache after the first. Sums are float32 in a fixed order: no atomics, the same bits on
-// every call.
+// size): 16 tokens, 2 of 8 experts (D = 4096, F = 11008, 8 experts used) read their 406 MB of gate and
+// up weights at 4.4 TB/s, a large device copy moving 5.2. A wavefront's product is a DotWave
+// (moe_dot.h, a few columns) or a MfmaWave (moe_mfma.h, up to 16), chosen on the host from the
+// columns an expert has on average. An expert with more columns than the form takes is worked
+// through in groups, its weights coming from the cache after the first. Sums are float32 in a fixed
+// order: no atomics, the same bits on every call.
 #include <cmath>
 
 #include "epilogue.h"
@@ -34,11 +35,6 @@ __device__ __forceinline__ int pair_at(const int* order, int i, int P) {
 // 2^-16: the quotient is at most 512 / 65536 = 1/128 too large, less than 1/k.
 __device__ __forceinline__ int token_of(int p, int m) { return (p * m) >> 16; }
 
-// Wavefronts per SIMD that a gated kernel's registers are held to: 4, or 2 where LDS (staging and
-// sums, per wavefront) leaves no room for 16 wavefronts per compute unit.
-template <class W>
-constexpr int kMinWaves = 16 * (W::kLds + 4 * W::kCols * W::kRows) > 160 * 1024 ? 2 : 4;
-
 // A product's form: what its wavefronts are and how many a workgroup has.
 template <class Wave, int Waves>
 struct Form {
@@ -52,7 +48,7 @@ struct Form {
 // for each block (KW * RB = NW): as many as K has steps, so that a short K gives a wavefront a
 // step of its own rather than none.
 template <class W, int NW>
-__global__ __launch_bounds__(64 * NW, kMinWaves<W>) void moe_gated_kernel(
+__global__ __launch_bounds__(64 * NW, 4) void moe_gated_kernel(
     const void* __restrict__ tokens, const int* __restrict__ plan,
     const uint8_t* __restrict__ wrep, float* __restrict__ H, int M, int E, int k, int F, int K,
     int entries, int act, int kw_log2, int blocks, int km) {
@@ -338,32 +334,32 @@ auto with_down(const MoeShape& m, int64_t compute_units, F f) {
     return narrow ? f(Form<DotWave<8, 1, true>, 16>{})
                   : f(Form<DotWave<16, 1, true>, 16>{});
   const double c = columns_per_expert(m);
-  // The vector-ALU form for few columns. D = 2048: at 1.7 columns (8 tokens, 8 of 64 experts) 17.4
-  // us against the matrix unit's 19.1, at 2.8 (23 tokens, 6 of 64) 32.1 against 29.8. D = 4096: at
-  // 2.2 columns (8 tokens, 2 of 8, F = 4096) 20.1 against 22.3, at 4 (16 tokens, F = 11008) 59.5
-  // against 56.7, at 16 (64 tokens) 168 against 111.
+  // The vector-ALU form for few columns (graph replays, vector ALU against matrix unit). D = 2048:
+  // at 1.3 columns (4 tokens, 8 of 64 experts of F = 1024) 13.2 against 14.7 us, at 1.7 (8 tokens)
+  // 16.8 against 19.3, at 2.8 (23 tokens, 6 of 64, F = 1280) 30.9 against 30.6, at 8 (64 tokens) 52.7
+  // against 44.0. D = 4096: at 1.3 (4 tokens, 2 of 8, F = 11008) 33.8 against 47.4, at 3.2 (12
+  // tokens, 4 of 16, F = 4096) 41.7 against 43.1, at 4 (16 tokens, 2 of 8) 59.4 against 59.9, at 16
+  // (64 tokens) 168 against 101. Its step is twice the matrix unit's bytes per wavefront, which
+  // counts while loads in flight set the rate.
   if (narrow)
-    return c <= 2.2 ? f(Form<DotWave<8, 3, false>, 16>{})
-                    : f(Form<MfmaWave<1, 16, 2, 1>, 16>{});
-  return c <= 3.0 ? f(Form<DotWave<16, 4, false>, 16>{})
-                  : f(Form<MfmaWave<1, 16, 1, 1>, 16>{});
+    return c <= 2.7 ? f(Form<DotWave<8, 3, false>, 16>{})
+                    : f(Form<MfmaWave<1, 2>, 16>{});
+  return c <= 4.0 ? f(Form<DotWave<16, 4, false>, 16>{})
+                  : f(Form<MfmaWave<1>, 16>{});
 }
 
 }  // namespace
 
 hipError_t launch_moe_gated(const void* tokens, const int* plan, const void* w, float* H,
                             const MoeShape& m, int act, hipStream_t s) {
+  // One token: the vector ALU, from float32, one launch. Else the matrix unit: with one or two
+  // columns it takes what the vector-ALU form with up to 4 took (graph replays: 2 tokens, 2 of 8
+  // experts, D = 4096, F = 11008, 46 us both; 4 tokens 66.3 against 66.9), with 4 columns 95 against
+  // 107, and with 16 (64 tokens) 139 against 278. Two wavefronts per workgroup, so that each walks
+  // half of K: the prologue and the sum over wavefronts weigh less (4 and 8 tokens were slower by
+  // up to 8 %), while one per workgroup leaves the short K of small experts unsplit.
   if (moe_fused(m.M)) return launch_gated<DotWave<16, 1, true>, 4>(tokens, plan, w, H, m, act, s);
-  // Graph replays over weights beyond the cache, vector ALU / matrix unit with 8 columns / with 16:
-  // at 1.3 columns (4 tokens, 2 of 8 experts, D = 4096, F = 11008) 65.7 / 73.3 / 82.6 us; at 1.7 (8
-  // tokens, 8 of 64, D = 2048, F = 1024) 29.8 / 29.0; at 4 (16 tokens, 2 of 8) 107 / 94 / 105; at 8
-  // (64 tokens, 8 of 64) 82.7 / 59.9 / 51.7; at 16 (64 tokens, 2 of 8) 278 / 188 / 150. Two
-  // wavefronts per workgroup in the matrix-unit form (each walks more of K, so its prologue and
-  // the sum over wavefronts weigh less): 91 us against 97 with 4 and 105 with 8 at 4 columns.
-  const double c = columns_per_expert(m);
-  if (c <= 1.6) return launch_gated<DotWave<16, 4, false>, 4>(tokens, plan, w, H, m, act, s);
-  if (c <= 6.0) return launch_gated<MfmaWave<2, 8>, 2>(tokens, plan, w, H, m, act, s);
-  return launch_gated<MfmaWave<2, 16>, 2>(tokens, plan, w, H, m, act, s);
+  return launch_gated<MfmaWave<2>, 2>(tokens, plan, w, H, m, act, s);
 }
 
 hipError_t launch_moe_down(const void* tokens, const int* plan, const float* weights,

@@ -118,6 +118,13 @@ def test_workspace_of_the_gated_product():
     assert mmq.mmq_gated_workspace_bytes(77, 688, 4096) == 0
 
 
+def test_pairs_to_tokens_by_multiplication():
+    """The kernels' p / k, (p * (65535 // k + 1)) >> 16, for every pair of every plan."""
+    for k in range(1, mmq.MOE_MAX_SLOTS + 1):
+        m = 65535 // k + 1
+        assert all((p * m) >> 16 == p // k for p in range(mmq.MOE_MAX_PAIRS)), k
+
+
 def test_gated_experts_grid_limit():
     # 8 experts, ceil(F/16) = 2^20: 2^23 in all
     a = [4, 8, 2, 1 << 24, 256, P, P, P, P, P, 2, None]
