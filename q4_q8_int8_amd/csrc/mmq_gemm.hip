@@ -509,8 +509,22 @@ __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
     float* C = static_cast<float*>(out) + (size_t)sp * (size_t)M * (size_t)N;
     const int j0c = wt * 32;
     const int rr = lane >> 3, c4 = lane & 7;  // read-back: rows rr + 8k, columns 4*c4..+3
+    bool vec = false;
+    float4 bias4, res4[4];  // of the lane's columns; of the rows of a tile, read ahead of its sums
+    if constexpr (EPI != kEpiNone) {
+      vec = wt_ok && (N & 3) == 0 && j0c + 4 * c4 + 3 < N;
+      if (vec) bias4 = epi_bias<EPI>(epi, j0c + 4 * c4);
+    }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
+      if constexpr (EPI != kEpiNone) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = m0 + t * 32 + rr + 8 * k;
+          if (vec && i < M)
+            res4[k] = epi_residual<EPI>(epi, (size_t)i * N + j0c + 4 * c4);
+        }
+      }
       float* tile = reinterpret_cast<float*>(smem) + ((t & 1) * NW + wave) * (32 * TS);
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -530,7 +544,7 @@ __global__ __launch_bounds__(NW * 64, NW >= 8 ? 1 : 2) void mmq_kernel(
           const size_t at = (size_t)i * N + j;
           float* p = C + at;
           if ((N & 3) == 0 && j + 3 < N) {
-            *reinterpret_cast<float4*>(p) = epi_four<EPI>(epi, v, at, j);
+            *reinterpret_cast<float4*>(p) = epi_four<EPI>(epi, v, bias4, res4[k]);
           } else {
             if (j + 0 < N) p[0] = epi_one<EPI>(epi, v.x, at, j);
             if (j + 1 < N) p[1] = epi_one<EPI>(epi, v.y, at + 1, j + 1);
@@ -591,7 +605,8 @@ __global__ __launch_bounds__(256) void reduce_splits_kernel(const float* __restr
       a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
     const int j = EPI == kEpiNone ? 0 : (int)(i % N);
-    *reinterpret_cast<float4*>(C + i) = epi_four<EPI>(epi, a, (size_t)i, j);
+    *reinterpret_cast<float4*>(C + i) =
+        epi_four<EPI>(epi, a, epi_bias<EPI>(epi, j), epi_residual<EPI>(epi, (size_t)i));
   } else {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;

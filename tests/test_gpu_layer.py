@@ -132,11 +132,33 @@ def test_activations_at_the_ends():
         mmq.mmq_q4K_f32_epilogue(M, N, K, xd, rep, C, bias=bias, act=mmq.ACTIVATIONS[act])
         got, want = host(C)[0].astype(np.float64), ref.numpy()
         assert np.array_equal(np.isnan(got), np.isnan(want)), act
-        # 2^-20 relative, and 3e-37: where e^-v overflows (v < -88.72) the result is -0 for at
-        # most 88.73 e^-88.72 = 2.7e-37
-        ok = np.isnan(want) | (got == want) | (np.abs(got - want) <= 2.0 ** -20 * np.abs(want)
-                                               + 3e-37)
+        # 2^-20 relative; and where e^v is below 2^-126 (v < -87.34) it is taken as 0, for a result
+        # of at most 87.34 * 2^-126 = 1.03e-36
+        with np.errstate(invalid="ignore"):
+            ok = np.isnan(want) | (got == want) | (np.abs(got - want) <= 2.0 ** -20 * np.abs(want)
+                                                   + 1.1e-36)
         assert ok.all(), (act, b[~ok], got[~ok], want[~ok])
+
+
+def test_activations_over_their_range():
+    """Every activation at 4096 values of the sum, fed through the bias (the product is 0): errors
+    against float64 within 2^-21 of max(|v|, 1), eight half units: the exponential and reciprocal, one
+    unit each, the roundings of argument, sum and products, and gelu's fit of 2.3e-7 of a tail whose
+    product with v is at most 0.17."""
+    M, N, K = 1, 4096, 256
+    v = np.concatenate([np.linspace(-20, 20, 2048), np.random.default_rng(0).standard_normal(1024),
+                        np.geomspace(1e-6, 10, 512), -np.geomspace(1e-6, 10, 512)])
+    v = v.astype(np.float32)
+    w = lu.weights(N, K, 1)
+    C, bias, rep = f32(M, N), to_dev(v), gpu_repack(w, N, K)
+    x = torch.zeros(M, K, device="cuda")
+    for act in ("silu", "gelu", "gelu_tanh"):
+        mmq.mmq_q4K_f32_epilogue(M, N, K, x, rep, C, bias=bias, act=mmq.ACTIVATIONS[act])
+        want = lo.act(v.astype(np.float64), act)
+        lu.assert_close(host(C)[0], want, 2.0 ** -21 * np.maximum(np.abs(v), 1.0), what=act)
+        # and relative to the value itself near 0, where it is v / 2
+        near = np.abs(v) < 0.1
+        assert np.all(np.abs(host(C)[0] - want)[near] <= 2.0 ** -20 * np.abs(want)[near]), act
 
 
 # ---------------------------------------------------------------- the gated product
