@@ -26,6 +26,17 @@ static __device__ __forceinline__ float buf_load_f32(__amdgpu_buffer_rsrc_t r, u
 static __device__ __forceinline__ float2 buf_load_f32x2(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
 }
+// Loads of data that is read once (the "nt" bit of the instruction: the caches are told not to keep
+// the line).
+constexpr int kReadOnce = 2;
+template <int AUX>
+static __device__ __forceinline__ v4i buf_load16_aux(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, AUX));
+}
+template <int AUX>
+static __device__ __forceinline__ uint2 buf_load8_aux(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, AUX));
+}
 // The same descriptor as four SGPRs, for the direct-to-LDS load below.
 static __device__ __forceinline__ v4i make_rsrc_sgpr(const void* p, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);

@@ -334,17 +334,18 @@ auto with_down(const MoeShape& m, int64_t compute_units, F f) {
     return narrow ? f(Form<DotWave<8, 1, true>, 16>{})
                   : f(Form<DotWave<16, 1, true>, 16>{});
   const double c = columns_per_expert(m);
-  // The vector-ALU form for few columns (graph replays, vector ALU against matrix unit). D = 2048:
-  // at 1.3 columns (4 tokens, 8 of 64 experts of F = 1024) 13.2 against 14.7 us, at 1.7 (8 tokens)
-  // 16.8 against 19.3, at 2.8 (23 tokens, 6 of 64, F = 1280) 30.9 against 30.6, at 8 (64 tokens) 52.7
-  // against 44.0. D = 4096: at 1.3 (4 tokens, 2 of 8, F = 11008) 33.8 against 47.4, at 3.2 (12
-  // tokens, 4 of 16, F = 4096) 41.7 against 43.1, at 4 (16 tokens, 2 of 8) 59.4 against 59.9, at 16
-  // (64 tokens) 168 against 101. Its step is twice the matrix unit's bytes per wavefront, which
-  // counts while loads in flight set the rate.
+  // The vector-ALU form for few columns (graph replays over weights beyond the cache, vector ALU
+  // against matrix unit). D = 2048: at 1.2 columns (4 tokens, 8 of 64 experts of F = 1024) 13.2
+  // against 14.7 us, at 1.5 (8 tokens) 16.8 against 19.3, at 2.4 (23 tokens, 6 of 64, F = 1280) 30.9
+  // against 30.6 (29.5 against 24.9 while the weights fit the cache), at 8 (64 tokens) 52.7 against
+  // 44.0. D = 4096: at 1.5 (4 tokens, 2 of 8, F = 11008) 33.8 against 47.4, at 3.1 (12 tokens, 4 of
+  // 16, F = 4096) 41.7 against 43.1, at 4 (16 tokens, 2 of 8) 57.8 against 59.9, at 16 (64 tokens) 168
+  // against 101. Its step is twice the matrix unit's bytes per wavefront, which counts while loads
+  // in flight set the rate.
   if (narrow)
-    return c <= 2.7 ? f(Form<DotWave<8, 3, false>, 16>{})
+    return c <= 2.0 ? f(Form<DotWave<8, 3, false>, 16>{})
                     : f(Form<MfmaWave<1, 2>, 16>{});
-  return c <= 4.0 ? f(Form<DotWave<16, 4, false>, 16>{})
+  return c <= 5.0 ? f(Form<DotWave<16, 4, false>, 16>{})
                   : f(Form<MfmaWave<1>, 16>{});
 }
 
@@ -359,7 +360,10 @@ hipError_t launch_moe_gated(const void* tokens, const int* plan, const void* w, 
   // half of K: the prologue and the sum over wavefronts weigh less (4 and 8 tokens were slower by
   // up to 8 %), while one per workgroup leaves the short K of small experts unsplit.
   if (moe_fused(m.M)) return launch_gated<DotWave<16, 1, true>, 4>(tokens, plan, w, H, m, act, s);
-  return launch_gated<MfmaWave<2>, 2>(tokens, plan, w, H, m, act, s);
+  // above 8 columns on average some experts have more than 16: their weights are read again
+  return columns_per_expert(m) <= 8.0
+             ? launch_gated<MfmaWave<2, 1, true>, 2>(tokens, plan, w, H, m, act, s)
+             : launch_gated<MfmaWave<2>, 2>(tokens, plan, w, H, m, act, s);
 }
 
 hipError_t launch_moe_down(const void* tokens, const int* plan, const float* weights,

@@ -461,6 +461,29 @@ def test_many_experts():
                         *lu.experts_down(H, ids, wts, ex.down, None))
 
 
+def test_expert_weights_past_4_gib():
+    """The last of 512 experts starts 4.3 GB into the weights."""
+    M, E, k, D, F = 2, 512, 2, 4096, 1840
+    n = mmq.mmq_q4K_pair_bytes(F, D)
+    assert (E - 1) * n > 2 ** 32
+    w_in = torch.empty(E * n, dtype=torch.uint8, device="cuda")   # only two experts are written
+    gate = {e: lu.weights(F, D, 2 * e) for e in (0, E - 1)}
+    up = {e: lu.weights(F, D, 2 * e + 1) for e in (0, E - 1)}
+    for e in gate:
+        mmq.repack_q4_K_pair(to_dev(gate[e]), to_dev(up[e]), F, D, w_in[e * n:(e + 1) * n])
+    x = synth.activations("normal", M, D, 3)
+    ids = np.array([[0, E - 1], [E - 1, -1]], np.int32)
+    H = f32(M * k, F)
+    say("experts past 4 GiB")
+    mmq.mmq_q4K_moe_gated(M, E, k, F, D, to_dev(x), plan_of(ids, E), w_in, H,
+                          raw(mmq.mmq_q8_1_bytes(M, D)))
+    got = host(H)
+    for p, (t, e) in enumerate(((0, 0), (0, E - 1), (1, E - 1))):
+        (G, TG), (U, TU) = lu.product(x[t:t + 1], gate[e]), lu.product(x[t:t + 1], up[e])
+        want, err = lo.gated(G, TG, U, TU, lu.BAR, "silu")
+        lu.assert_close(got[p:p + 1], want, err)
+
+
 def test_moe_gated_one_expert_per_token_is_the_gated_product():
     """With one expert every pair is a row of the dense gated product, within both bounds."""
     M, D, F = 16, 1024, 256
