@@ -77,7 +77,7 @@ int mmq_q4K_f32_epilogue(int64_t M, int64_t N, int64_t K, const float* x, const 
  * F <= 2^29.
  * repack_q4_K_pair: the records of repack_q4_K over the packed rows: packed row 16 b + r is row
  * 8 b + r of w_gate for r < 8, row 8 b + r - 8 of w_up for r >= 8; rows past F are zero, up to a
- * multiple of 32 packed rows. Run once per pair. Errors as repack_q4_K.
+ * multiple of 32 packed rows. Run once per pair; ceil(F/16) * (K/256) < 2^24. Errors as repack_q4_K.
  */
 int mmq_q4K_pair_bytes(int64_t F, int64_t K, size_t* bytes);
 int repack_q4_K_pair(const void* w_gate, const void* w_up, int64_t F, int64_t K, void* w_pair,
@@ -100,7 +100,7 @@ int mmq_q4K_f32_gated(int64_t M, int64_t F, int64_t K, const float* x, const voi
 
 /* ---------------------------------------------------------------- mixture of experts */
 
-/* Limits of a plan and of the products that read it (the router alone takes any M). */
+/* Limits of a plan and of the products that read it (the router alone takes up to 2^25 tokens). */
 #define MMQ_MOE_MAX_TOKENS 64
 #define MMQ_MOE_MAX_PAIRS 512   /* M * k */
 #define MMQ_MOE_MAX_EXPERTS 512
@@ -135,8 +135,8 @@ int mmq_moe_plan(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* p
  *                      that sum is 0)
  * A logit of -inf or NaN is never chosen and weighs nothing (a masked expert); a token with fewer
  * than k others gets id -1 and weight 0 in the slots that are left. Where the greatest logit is
- * +inf, the experts that have it share the softmax. plan may be NULL (then any M >= 1, M * E <
- * 2^40, M <= 2^30); otherwise it is written as mmq_moe_plan would.
+ * +inf, the experts that have it share the softmax. plan may be NULL (then 1 <= M <= 2^25);
+ * otherwise it is written as mmq_moe_plan would.
  * 1 <= E <= 512, 1 <= k <= min(E, 64).
  */
 int mmq_moe_route(int64_t M, int64_t E, int64_t k, const float* logits, int32_t score,
@@ -146,7 +146,8 @@ int mmq_moe_route(int64_t M, int64_t E, int64_t k, const float* logits, int32_t 
  * mmq_q4K_moe_gated: H[p][F] = act(x[t] Wg(e)^T) * (x[t] Wu(e)^T) for every pair p = t*k + s of
  * the plan with an expert e; rows of H of pairs without one are left as they were. x float32
  * [M][D]; w_pairs: E repacked pairs (F, D) one behind the other; q8: scratch of
- * mmq_q8_1_bytes(M, D) bytes. Each used expert's weights are read once, for all its pairs.
+ * mmq_q8_1_bytes(M, D) bytes (not written for one token, whose values the product quantizes
+ * itself). Each used expert's weights are read once for up to 16 of its pairs.
  * M <= 64, M*k <= 512, E <= 512, D % 256 == 0, D <= 2^24, min(E, M*k) * ceil(F/16) < 2^23.
  * Errors: MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP.
  */
@@ -159,8 +160,8 @@ int mmq_q4K_moe_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, con
  * over the plan's pairs p = t*k + s; slots without an expert add nothing, and a token without any
  * gets its residual (0 if residual is NULL). H float32 [M*k][F] (rows of pairs without an expert
  * are not used); weights float32 [M][k]; w_down: E repacked q4_K matrices (D, F) one behind the
- * other; q8: scratch of mmq_q8_1_bytes(M*k, F) bytes; residual may be out itself. M <= 64,
- * M*k <= 512, E <= 512, F % 256 == 0, F <= 2^24, M*k*F < 2^31, D <= 2^30. Errors as
+ * other; q8: scratch of mmq_q8_1_bytes(M*k, F) bytes, as above; residual may be out itself.
+ * M <= 64, M*k <= 512, E <= 512, F % 256 == 0, F <= 2^24, M*k*F < 2^31, D <= 2^25. Errors as
  * mmq_q4K_moe_gated.
  */
 int mmq_q4K_moe_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const float* H,

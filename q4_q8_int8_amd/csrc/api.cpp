@@ -695,8 +695,9 @@ int repack_q4_K_pair(const void* w_gate, const void* w_up, int64_t F, int64_t K,
   size_t nb;
   int st = mmq_q4K_pair_bytes(F, K, &nb);
   if (st) return st;
-  if ((__int128)((F + 15) / 16) * (K / MMQ_QK_K) >= ((__int128)1 << 31))
-    return fail(MMQ_E_SHAPE, "repack_q4_K_pair takes ceil(F/16)*(K/256) below 2^31");
+  // a workgroup of 256 work-items each, on a grid of fewer than 2^32
+  if ((__int128)((F + 15) / 16) * (K / MMQ_QK_K) >= ((__int128)1 << 24))
+    return fail(MMQ_E_SHAPE, "repack_q4_K_pair takes ceil(F/16)*(K/256) below 2^24");
   if (!w_gate || !w_up || !w_pair) return fail(MMQ_E_ARG, "null device pointer");
   if (!aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_pair))
     return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");

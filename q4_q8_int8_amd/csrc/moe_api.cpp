@@ -27,6 +27,9 @@ int fail(int status, const char* fmt, ...) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
+// A grid holds fewer than 2^32 work-items: the router launches 64 per token, the down product at most
+// 64 per output column (1024 per 16 columns; with 8, as many workgroups as compute units).
+constexpr int64_t kMaxRouted = (int64_t)1 << 25, kMaxDown = (int64_t)1 << 25;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
 constexpr int64_t kMaxSlots = MMQ_MOE_MAX_SLOTS;
 static_assert(MMQ_MOE_MAX_TOKENS == mmq::kMoeMaxTokens, "limits");
@@ -41,7 +44,7 @@ int check_routing(int64_t M, int64_t E, int64_t k, bool planned) {
   if (E > mmq::kMoeMaxExperts) return fail(MMQ_E_SHAPE, "E = %lld is above 512", (long long)E);
   if (k > E || k > kMaxSlots)
     return fail(MMQ_E_SHAPE, "k = %lld is above min(E, %lld)", (long long)k, (long long)kMaxSlots);
-  if (M > kMaxDim) return fail(MMQ_E_SHAPE, "M above 2^30");
+  if (M > kMaxRouted) return fail(MMQ_E_SHAPE, "M above 2^25");
   if (planned && (M > mmq::kMoeMaxTokens || M * k > mmq::kMoeMaxPairs))
     return fail(MMQ_E_SHAPE, "a plan is for few tokens: M <= 64 and M*k <= 512 (%lld, %lld)",
                 (long long)M, (long long)(M * k));
@@ -119,7 +122,7 @@ int check_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, int32_t a
 
 int check_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F) {
   const int st = check_routing(M, E, k, true);
-  return st ? st : check_product("D", D, "F", F, M * k, kMaxDim);
+  return st ? st : check_product("D", D, "F", F, M * k, kMaxDown);
 }
 
 // The layer's workspace: each part at a 256-byte boundary. H is quantized into `q8`, which x used

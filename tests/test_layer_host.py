@@ -194,6 +194,17 @@ def test_expert_products_check_shapes_and_pointers():
                         None) == mmq.MMQ_E_SHAPE
 
 
+def test_grids_stay_below_2_to_the_32_work_items():
+    assert mmq.raw_call("mmq_moe_route", (1 << 25) + 1, 1, 1, P, 0, 1, P, P, None,
+                        None) == mmq.MMQ_E_SHAPE
+    assert mmq.raw_call("mmq_q4K_moe_down", 1, 1, 1, (1 << 25) + 1, 256, P, P, P, P, None, P, P,
+                        None) == mmq.MMQ_E_SHAPE
+    # 2^24 records of 256 work-items
+    assert mmq.raw_call("repack_q4_K_pair", P, P, 1 << 28, 256, P, None) == mmq.MMQ_E_SHAPE
+    assert mmq.raw_call("mmq_q4K_moe_gated", 1, 1, 1, 1 << 27, 256, P, P, P, P, P, 2,
+                        None) == mmq.MMQ_E_SHAPE
+
+
 def test_layer_checks_its_workspace():
     need = mmq.mmq_moe_workspace_bytes(2, 8, 2, 256, 256)
     call = [2, 8, 2, 256, 256, P, P, 0, 1, P, 2, P, None, P, P, need - 1, None]
