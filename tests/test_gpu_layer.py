@@ -579,17 +579,49 @@ def test_decoder_block_in_a_graph(M):
         assert np.array_equal(host(out), want), seed
 
 
-def test_layer_on_another_stream():
+def test_layer_on_two_streams_at_once():
     M, E, k, D, F = 3, 8, 2, 512, 256
     ex = Experts(E, D, F)
+    runs = []
+    for seed in (3, 4):
+        x = to_dev(synth.activations("normal", M, D, seed))
+        logits = to_dev(np.random.default_rng(seed).standard_normal((M, E)).astype(np.float32))
+        want = host(layer(ex, x, logits, k, "sigmoid", True)[0])
+        out, ws = f32(M, D), raw(mmq.mmq_moe_workspace_bytes(M, E, k, D, F))
+        runs.append((x, logits, out, ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    say("layer on two streams", (M, E, k, D, F))
+    for _ in range(20):                               # a workspace of its own for each stream
+        for x, logits, out, ws, _, s in runs:
+            mmq.mmq_q4K_moe(M, E, k, D, F, x, logits, ex.w_in, ex.w_out, out, ws,
+                            score=mmq.SCORES["sigmoid"], stream=s)
+    torch.cuda.synchronize()
+    for _, _, out, _, want, _ in runs:
+        assert np.array_equal(host(out), want)
+
+
+def test_a_plan_of_nonsense_selects_nothing():
+    """The products check what they read of a plan: entries outside its own sizes have no pairs."""
+    M, E, k, D, F = 5, 8, 2, 512, 256
+    ex = Experts(E, D, F)
+    P, entries = M * k, min(E, M * k)
     x = to_dev(synth.activations("normal", M, D, 3))
-    logits = to_dev(np.random.default_rng(4).standard_normal((M, E)).astype(np.float32))
-    want = host(layer(ex, x, logits, k, "sigmoid", True)[0])
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
-    out, ws = layer(ex, x, logits, k, "sigmoid", True, stream=s)
-    s.synchronize()
-    assert np.array_equal(out.cpu().numpy(), want)
+    res, w = to_dev(synth.activations("normal", M, D, 4)), f32(M, k).fill_(1.0)
+    bad = [(E, 0, 1), (-1, 0, 1), (0, P + 1, 0), (0, -1, 2), (0, 0, P + 1), (0, 0, -1),
+           (0, P, 1), (1 << 30, 1 << 30, 1 << 30)]
+    for used in (entries, entries + 1, -1, 1 << 30):
+        plan = np.full(4 + 4 * entries + P, (1 << 31) - 1, np.int32)
+        plan[0] = used
+        for u in range(entries):
+            plan[4 + 4 * u:7 + 4 * u] = bad[u % len(bad)]
+        H, out = f32(P, F), f32(M, D)
+        say("nonsense plan", used)
+        mmq.mmq_q4K_moe_gated(M, E, k, F, D, x, to_dev(plan), ex.w_in, H,
+                              raw(mmq.mmq_q8_1_bytes(M, D)))
+        assert np.isnan(host(H)).all()
+        mmq.mmq_q4K_moe_down(M, E, k, D, F, H.fill_(1.0), to_dev(plan), w, ex.w_out, out,
+                             raw(mmq.mmq_q8_1_bytes(P, F)), residual=res)
+        assert np.array_equal(host(out), host(res))
 
 
 def test_results_repeat_bit_for_bit():
