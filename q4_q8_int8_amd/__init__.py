@@ -163,16 +163,17 @@ class MMQArgumentError(ValueError):
     """A tensor handed to a wrapper does not fit the call (raised before any launch)."""
 
 
-def _dev(t, name: str, nbytes: int, dtype=None) -> int:
+def _dev(t, name: str, nbytes: int, dtype=None, here: int | None = None) -> int:
     """Device pointer of tensor t after checking that the call may use it: a contiguous CUDA
     tensor on the current device, of `dtype` when given, holding at least `nbytes` bytes.
     The C ABI takes bare pointers and cannot check buffer sizes itself, so an undersized or
-    mistyped buffer is refused here rather than read or written out of bounds."""
+    mistyped buffer is refused here rather than read or written out of bounds. `here`: the current
+    device, for a call that checks several tensors."""
     # the whole check in one expression: a decoding step makes tens of these calls, and the host
     # side of a call is longer than its kernel (0.4 us here against 0.8 us for the checks below)
     if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype == dtype)
             and t.is_contiguous() and t.nbytes >= nbytes
-            and t.get_device() == torch._C._cuda_getDevice()):
+            and t.get_device() == (_here() if here is None else here)):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise MMQArgumentError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
@@ -191,17 +192,18 @@ def _dev(t, name: str, nbytes: int, dtype=None) -> int:
     return t.data_ptr()
 
 
-def _f32():
-    return torch.float32
+def _here() -> int | None:
+    """The current device's index (0.1 us, a quarter of _dev: asked for once per call)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:  # no GPU: then no tensor is on one
+        return None
 
 
-def _i32():
-    return torch.int32
-
-
-def _stream(stream) -> int | None:
+def _stream(stream, here: int | None = None) -> int | None:
     if stream is None:  # (torch.cuda.current_stream() makes a Stream object: 2.9 us against 0.2)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if here is None
+                                                  else here)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -251,17 +253,18 @@ def mmq_q4K_repacked_bytes(N: int, K: int) -> int:
 
 
 # ---------------------------------------------------------------- the hot path
-def _gemm_ptrs(M: int, N: int, K: int, q8, w_rep, C):
-    return (_dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K)),
-            _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K)),
-            _dev(C, "C", 4 * M * N, _f32()))
+def _gemm_ptrs(M: int, N: int, K: int, q8, w_rep, C, here: int | None = None):
+    return (_dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K), here=here),
+            _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K), here=here),
+            _dev(C, "C", 4 * M * N, torch.float32, here))
 
 
 def quantize_q8_1(x, M: int, K: int, q8, stream=None) -> None:
     """x: f32 [M, K] device tensor; q8: device buffer of mmq_q8_1_bytes(M, K) bytes."""
-    xp = _dev(x, "x", 4 * M * K, _f32())
-    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
-    _check("quantize_q8_1", _lib.quantize_q8_1(xp, M, K, qp, _stream(stream)))
+    here = _here()
+    xp = _dev(x, "x", 4 * M * K, torch.float32, here)
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K), here=here)
+    _check("quantize_q8_1", _lib.quantize_q8_1(xp, M, K, qp, _stream(stream, here)))
 
 
 def repack_q4_K(w_q4K, N: int, K: int, w_rep, stream=None) -> None:
@@ -310,10 +313,11 @@ def mmq_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def mmq_q4K_f32(M: int, N: int, K: int, x, w_rep, C, stream=None) -> None:
     """Few tokens (M <= 128): C[M, N] from f32 activations x [M, K], quantized in the GEMM."""
-    xp = _dev(x, "x", 4 * M * K, _f32())
-    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
-    cp = _dev(C, "C", 4 * M * N, _f32())
-    _check("mmq_q4K_f32", _lib.mmq_q4K_f32(M, N, K, xp, rp, cp, _stream(stream)))
+    here = _here()
+    xp = _dev(x, "x", 4 * M * K, torch.float32, here)
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K), here=here)
+    cp = _dev(C, "C", 4 * M * N, torch.float32, here)
+    _check("mmq_q4K_f32", _lib.mmq_q4K_f32(M, N, K, xp, rp, cp, _stream(stream, here)))
 
 
 def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, j0: int,
@@ -322,16 +326,16 @@ def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
     """S: int32 device tensor [K/32, i1-i0, j1-j0] of per-block integer dot products."""
     qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
     rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
-    sp = _dev(S, "S", 4 * (K // QK8) * max(i1 - i0, 0) * max(j1 - j0, 0), _i32())
+    sp = _dev(S, "S", 4 * (K // QK8) * max(i1 - i0, 0) * max(j1 - j0, 0), torch.int32)
     _check("mmq_q4K_q8_1_blockdots",
            _lib.mmq_q4K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp,
                                        _stream(stream), _opts(force_tile, lds_budget)))
 
 
 # ---------------------------------------------------------------- the product's epilogue
-def _epi(M: int, N: int, bias, residual, act: int):
-    bp = None if bias is None else _dev(bias, "bias", 4 * N, _f32())
-    rp = None if residual is None else _dev(residual, "residual", 4 * M * N, _f32())
+def _epi(M: int, N: int, bias, residual, act: int, here: int):
+    bp = None if bias is None else _dev(bias, "bias", 4 * N, torch.float32, here)
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * N, torch.float32, here)
     return ctypes.byref(mmq_epilogue(bp, rp, act, 0))
 
 
@@ -340,11 +344,12 @@ def mmq_q4K_q8_1_epilogue(M: int, N: int, K: int, q8, w_rep, C, bias=None, resid
                           lds_budget: int = 0, min_workgroups: int = 0, workspace=None,
                           splits: int = 0) -> None:
     """C[M, N] = act(product + bias[N]) + residual[M, N] (f32 tensors; residual may be C)."""
-    qp, rp, cp = _gemm_ptrs(M, N, K, q8, w_rep, C)
+    here = _here()
+    qp, rp, cp = _gemm_ptrs(M, N, K, q8, w_rep, C, here)
     wp, wb = _workspace(workspace)
     _check("mmq_q4K_q8_1_epilogue",
-           _lib.mmq_q4K_q8_1_epilogue(M, N, K, qp, rp, cp, _stream(stream),
-                                      _epi(M, N, bias, residual, act),
+           _lib.mmq_q4K_q8_1_epilogue(M, N, K, qp, rp, cp, _stream(stream, here),
+                                      _epi(M, N, bias, residual, act, here),
                                       _opts(force_tile, lds_budget, min_workgroups, wp, wb,
                                             splits)))
 
@@ -352,12 +357,13 @@ def mmq_q4K_q8_1_epilogue(M: int, N: int, K: int, q8, w_rep, C, bias=None, resid
 def mmq_q4K_f32_epilogue(M: int, N: int, K: int, x, w_rep, C, bias=None, residual=None,
                          act: int = MMQ_ACT_NONE, stream=None) -> None:
     """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
-    xp = _dev(x, "x", 4 * M * K, _f32())
-    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
-    cp = _dev(C, "C", 4 * M * N, _f32())
+    here = _here()
+    xp = _dev(x, "x", 4 * M * K, torch.float32, here)
+    rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K), here=here)
+    cp = _dev(C, "C", 4 * M * N, torch.float32, here)
     _check("mmq_q4K_f32_epilogue",
-           _lib.mmq_q4K_f32_epilogue(M, N, K, xp, rp, cp, _stream(stream),
-                                     _epi(M, N, bias, residual, act)))
+           _lib.mmq_q4K_f32_epilogue(M, N, K, xp, rp, cp, _stream(stream, here),
+                                     _epi(M, N, bias, residual, act, here)))
 
 
 # ---------------------------------------------------------------- the gated product
@@ -387,23 +393,25 @@ def mmq_q4K_q8_1_gated(M: int, F: int, K: int, q8, w_pair, H, act: int = MMQ_ACT
                        stream=None, force_tile: int = MMQ_TILE_AUTO, lds_budget: int = 0,
                        min_workgroups: int = 0, workspace=None, splits: int = 0) -> None:
     """H[M, F] (f32) = act(x Wg^T) * (x Wu^T), q8 (M x K) and a repacked pair (F x K)."""
-    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
-    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K))
-    hp = _dev(H, "H", 4 * M * F, _f32())
+    here = _here()
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K), here=here)
+    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K), here=here)
+    hp = _dev(H, "H", 4 * M * F, torch.float32, here)
     wp, wb = _workspace(workspace)
     _check("mmq_q4K_q8_1_gated",
-           _lib.mmq_q4K_q8_1_gated(M, F, K, qp, pp, hp, _stream(stream), act,
+           _lib.mmq_q4K_q8_1_gated(M, F, K, qp, pp, hp, _stream(stream, here), act,
                                    _opts(force_tile, lds_budget, min_workgroups, wp, wb, splits)))
 
 
 def mmq_q4K_f32_gated(M: int, F: int, K: int, x, w_pair, H, act: int = MMQ_ACT_SILU,
                       stream=None) -> None:
     """Few tokens (M <= 128): the same from f32 activations x [M, K]."""
-    xp = _dev(x, "x", 4 * M * K, _f32())
-    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K))
-    hp = _dev(H, "H", 4 * M * F, _f32())
+    here = _here()
+    xp = _dev(x, "x", 4 * M * K, torch.float32, here)
+    pp = _dev(w_pair, "w_pair", _sized(mmq_q4K_pair_bytes, F, K), here=here)
+    hp = _dev(H, "H", 4 * M * F, torch.float32, here)
     _check("mmq_q4K_f32_gated",
-           _lib.mmq_q4K_f32_gated(M, F, K, xp, pp, hp, _stream(stream), act))
+           _lib.mmq_q4K_f32_gated(M, F, K, xp, pp, hp, _stream(stream, here), act))
 
 
 # ---------------------------------------------------------------- mixture of experts
@@ -415,34 +423,38 @@ def mmq_moe_plan_bytes(M: int, E: int, k: int) -> int:
 
 def mmq_moe_plan(M: int, E: int, k: int, ids, plan, stream=None) -> None:
     """plan (int32, mmq_moe_plan_bytes) from ids int32 [M, k]; an id outside [0, E) is no expert."""
-    ip = _dev(ids, "ids", 4 * M * k, _i32())
-    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
-    _check("mmq_moe_plan", _lib.mmq_moe_plan(M, E, k, ip, pp, _stream(stream)))
+    here = _here()
+    ip = _dev(ids, "ids", 4 * M * k, torch.int32, here)
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), torch.int32, here)
+    _check("mmq_moe_plan", _lib.mmq_moe_plan(M, E, k, ip, pp, _stream(stream, here)))
 
 
 def mmq_moe_route(M: int, E: int, k: int, logits, ids, weights, plan=None,
                   score: int = MMQ_SCORE_SOFTMAX, renorm: bool = True, stream=None) -> None:
     """The k experts of the greatest logits [M, E] (f32): ids int32 [M, k], weights f32 [M, k] and,
     for at most 64 tokens, the plan of the experts' products (int32, mmq_moe_plan_bytes)."""
-    lp = _dev(logits, "logits", 4 * M * E, _f32())
-    ip = _dev(ids, "ids", 4 * M * k, _i32())
-    wp = _dev(weights, "weights", 4 * M * k, _f32())
-    pp = None if plan is None else _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
+    here = _here()
+    lp = _dev(logits, "logits", 4 * M * E, torch.float32, here)
+    ip = _dev(ids, "ids", 4 * M * k, torch.int32, here)
+    wp = _dev(weights, "weights", 4 * M * k, torch.float32, here)
+    pp = (None if plan is None
+          else _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), torch.int32, here))
     _check("mmq_moe_route",
-           _lib.mmq_moe_route(M, E, k, lp, score, int(renorm), ip, wp, pp, _stream(stream)))
+           _lib.mmq_moe_route(M, E, k, lp, score, int(renorm), ip, wp, pp, _stream(stream, here)))
 
 
 def mmq_q4K_moe_gated(M: int, E: int, k: int, F: int, D: int, x, plan, w_pairs, H, q8,
                       act: int = MMQ_ACT_SILU, stream=None) -> None:
     """H[M*k, F] (f32): per (token, slot) pair of the plan the gated product of its expert.
     w_pairs: E repacked pairs (mmq_q4K_pair_bytes(F, D) each); q8: scratch, mmq_q8_1_bytes(M, D)."""
-    xp = _dev(x, "x", 4 * M * D, _f32())
-    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
-    wp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D))
-    hp = _dev(H, "H", 4 * M * k * F, _f32())
-    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, D))
+    here = _here()
+    xp = _dev(x, "x", 4 * M * D, torch.float32, here)
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), torch.int32, here)
+    wp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D), here=here)
+    hp = _dev(H, "H", 4 * M * k * F, torch.float32, here)
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, D), here=here)
     _check("mmq_q4K_moe_gated",
-           _lib.mmq_q4K_moe_gated(M, E, k, F, D, xp, pp, wp, hp, qp, act, _stream(stream)))
+           _lib.mmq_q4K_moe_gated(M, E, k, F, D, xp, pp, wp, hp, qp, act, _stream(stream, here)))
 
 
 def mmq_q4K_moe_down(M: int, E: int, k: int, D: int, F: int, H, plan, weights, w_down, out, q8,
@@ -450,15 +462,16 @@ def mmq_q4K_moe_down(M: int, E: int, k: int, D: int, F: int, H, plan, weights, w
     """out[M, D] (f32) = residual + per token the weighted sum over its slots of H[p] W(expert)^T.
     w_down: E repacked matrices (mmq_q4K_repacked_bytes(D, F) each); q8: scratch of
     mmq_q8_1_bytes(M*k, F) bytes; residual may be out."""
-    hp = _dev(H, "H", 4 * M * k * F, _f32())
-    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), _i32())
-    gp = _dev(weights, "weights", 4 * M * k, _f32())
-    wp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F))
-    op = _dev(out, "out", 4 * M * D, _f32())
-    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
-    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M * k, F))
+    here = _here()
+    hp = _dev(H, "H", 4 * M * k * F, torch.float32, here)
+    pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), torch.int32, here)
+    gp = _dev(weights, "weights", 4 * M * k, torch.float32, here)
+    wp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F), here=here)
+    op = _dev(out, "out", 4 * M * D, torch.float32, here)
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, torch.float32, here)
+    qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M * k, F), here=here)
     _check("mmq_q4K_moe_down",
-           _lib.mmq_q4K_moe_down(M, E, k, D, F, hp, pp, gp, wp, rp, op, qp, _stream(stream)))
+           _lib.mmq_q4K_moe_down(M, E, k, D, F, hp, pp, gp, wp, rp, op, qp, _stream(stream, here)))
 
 
 def mmq_moe_workspace_bytes(M: int, E: int, k: int, D: int, F: int) -> int:
@@ -473,17 +486,18 @@ def mmq_q4K_moe(M: int, E: int, k: int, D: int, F: int, x, logits, w_pairs, w_do
                 act: int = MMQ_ACT_SILU, residual=None, stream=None) -> None:
     """The whole layer for a few tokens: out[M, D] = residual + experts of x [M, D] chosen by the
     router's logits [M, E]. workspace: mmq_moe_workspace_bytes(M, E, k, D, F) bytes."""
-    xp = _dev(x, "x", 4 * M * D, _f32())
-    lp = _dev(logits, "logits", 4 * M * E, _f32())
-    gp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D))
-    dp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F))
-    op = _dev(out, "out", 4 * M * D, _f32())
-    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, _f32())
-    sp, sb = _dev(workspace, "workspace", _sized(mmq_moe_workspace_bytes, M, E, k, D, F)), \
-        workspace.numel() * workspace.element_size()
+    here = _here()
+    xp = _dev(x, "x", 4 * M * D, torch.float32, here)
+    lp = _dev(logits, "logits", 4 * M * E, torch.float32, here)
+    gp = _dev(w_pairs, "w_pairs", E * _sized(mmq_q4K_pair_bytes, F, D), here=here)
+    dp = _dev(w_down, "w_down", E * _sized(mmq_q4K_repacked_bytes, D, F), here=here)
+    op = _dev(out, "out", 4 * M * D, torch.float32, here)
+    rp = None if residual is None else _dev(residual, "residual", 4 * M * D, torch.float32, here)
+    sp = _dev(workspace, "workspace", _sized(mmq_moe_workspace_bytes, M, E, k, D, F), here=here)
+    sb = workspace.numel() * workspace.element_size()
     _check("mmq_q4K_moe",
            _lib.mmq_q4K_moe(M, E, k, D, F, xp, lp, score, int(renorm), gp, act, dp, rp, op, sp, sb,
-                            _stream(stream)))
+                            _stream(stream, here)))
 
 
 # ---------------------------------------------------------------- the q6_K variant
@@ -509,7 +523,7 @@ def repack_q6_K(w_q6K, N: int, K: int, w_rep, stream=None) -> None:
 def _gemm6_ptrs(M: int, N: int, K: int, q8, w_rep, C):
     return (_dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K)),
             _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K)),
-            _dev(C, "C", 4 * M * N, _f32()))
+            _dev(C, "C", 4 * M * N, torch.float32))
 
 
 def mmq_q6K_q8_1(M: int, N: int, K: int, q8, w_rep, C, stream=None) -> None:
@@ -533,7 +547,7 @@ def mmq_q6K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
     """S: int32 device tensor [K/16, i1-i0, j1-j0] of per-group integer dot products."""
     qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
     rp = _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K))
-    sp = _dev(S, "S", 4 * (K // 16) * max(i1 - i0, 0) * max(j1 - j0, 0), _i32())
+    sp = _dev(S, "S", 4 * (K // 16) * max(i1 - i0, 0) * max(j1 - j0, 0), torch.int32)
     _check("mmq_q6K_q8_1_blockdots",
            _lib.mmq_q6K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp, _stream(stream),
                                        _opts(force_tile)))
@@ -559,7 +573,7 @@ def mmq_f16_bytes(rows: int, K: int) -> int:
 
 def convert_f32_f16(x, M: int, K: int, x_f16, stream=None) -> None:
     """x: f32 [M, K] device tensor; x_f16: device buffer of mmq_f16_bytes(M, K) bytes."""
-    xp = _dev(x, "x", 4 * M * K, _f32())
+    xp = _dev(x, "x", 4 * M * K, torch.float32)
     hp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
     _check("convert_f32_f16", _lib.convert_f32_f16(xp, M, K, hp, _stream(stream)))
 
@@ -575,7 +589,7 @@ def gemm_f16(M: int, N: int, K: int, x_f16, w_f16, C, stream=None) -> None:
     """C[M, N] (f32 device tensor) = x_f16 [M, K] times w_f16 [N, K]^T, f32 accumulation."""
     xp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
     wp = _dev(w_f16, "w_f16", _sized(mmq_f16_bytes, N, K))
-    cp = _dev(C, "C", 4 * M * N, _f32())
+    cp = _dev(C, "C", 4 * M * N, torch.float32)
     _check("gemm_f16", _lib.gemm_f16(M, N, K, xp, wp, cp, _stream(stream)))
 
 

@@ -305,9 +305,11 @@ hipError_t launch_down(const void* tokens, const int* plan, const float* weights
                        const float* residual, float* out, const MoeShape& m, hipStream_t s) {
   auto kern = moe_down_kernel<W, NW>;
   const int64_t lds = down_lds<W, NW>(m);
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return e;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(kern, dim3((unsigned)((m.D + W::kRows - 1) / W::kRows)), dim3(64 * NW),
                      (size_t)lds, s, tokens, plan, weights, static_cast<const uint8_t*>(w),
                      residual, out, (int)m.M, (int)m.E, (int)m.k, (int)m.D, (int)m.F,
