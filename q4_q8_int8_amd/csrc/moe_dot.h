@@ -2,7 +2,7 @@
 // weight rows of one expert, integer dot products on v_dot4_i32_i8.
 //
 // A matrix instruction costs the same for one column as for sixteen, and the rescale of its
-// results too: per 16 rows and 32-block about 22 vector instructions. On the vector ALU a lane
+// results too: per 16 rows and 32-block about 20 vector instructions. On the vector ALU a lane
 // takes one row and half a super-block: per block 12 instructions to unpack the nibbles and make
 // the scales and 12 per column (8 dot products, 4 for the rescale), for 64 (row, block) pairs at a
 // time. Up to about 5 columns that is less, and with one token most experts have one column.

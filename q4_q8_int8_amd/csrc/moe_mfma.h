@@ -14,9 +14,9 @@
 // bf16 unit in exact pieces, which is faster there; here the f32 instruction has time to spare,
 // and needs no pieces: 40 vector instructions fewer per 32 rows and super-block.)
 //
-// Up to 16 columns cost what one does, about 150 vector instructions per super-block and 16 rows,
-// 128 of them per 32 rows the rescale. That is what bounds the form: at 16 tokens, 2 of 8 experts
-// (D = 4096, F = 11008) the vector ALU is 73 % busy while the weights come at 4.4 TB/s.
+// Up to 16 columns cost what one does, 165 vector instructions per super-block and 16 rows, 64 of
+// them the rescale. That bounds the form beside the memory: at 16 tokens, 2 of 8 experts (D = 4096, F =
+// 11008) the vector ALU is 67 % busy while the weights come at 4.3 to 4.9 TB/s.
 //
 // KS = 2: 8 weight rows and two super-blocks at a time. Operand rows 0..7 are the rows of the first
 // super-block and 8..15 the same rows of the second, operand columns 0..7 the columns of the first
