@@ -131,8 +131,9 @@ int mmq_moe_plan(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* p
  * mmq_moe_route: per token t the k experts of the greatest logits[t][0..E), in decreasing order,
  * equal logits in increasing order of expert, into ids[t][0..k), and their weights:
  *   MMQ_SCORE_SOFTMAX  e^(l_s - max) / sum over all E experts, or over the k chosen with renorm
- *   MMQ_SCORE_SIGMOID  1 / (1 + e^-l_s), divided by the sum over the k chosen with renorm (0 where
- *                      that sum is 0)
+ *   MMQ_SCORE_SIGMOID  1 / (1 + e^-l_s), divided by the sum over the k chosen with renorm: by the
+ *                      scores' ratios, however small they are, as long as the greatest of them is
+ *                      not 0 in float32 (a logit below -150 ln 2 = -103.97); then all weigh 0
  * A logit of -inf or NaN is never chosen and weighs nothing (a masked expert); a token with fewer
  * than k others gets id -1 and weight 0 in the slots that are left. Where the greatest logit is
  * +inf, the experts that have it share the softmax. plan may be NULL (then 1 <= M <= 2^25);

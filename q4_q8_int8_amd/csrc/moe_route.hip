@@ -63,6 +63,10 @@ __device__ __forceinline__ float exp_below(float v, float top) {
   return v == top ? 1.0f : expf(v - top);
 }
 
+// The least float32 whose sigmoid is not 0 in float32: e^v rounds to 0 below 2^-150, v = -150 ln 2 =
+// -103.972077. Below it normalised weights are 0: the sum of the scores is 0.
+constexpr float kLeastSigmoid = -0x1.9fe368p+6f;
+
 // One token. NV values per lane (E <= 64 NV). Lane s < k ends with slot s: its expert (-1: fewer
 // than k could be chosen) and weight.
 template <int NV>
@@ -115,7 +119,12 @@ __device__ void route_token(const float* __restrict__ logits, int E, int k, int 
     const float sum = wave_sum(all);
     weight = id >= 0 ? weight / sum : 0.0f;
   } else {
-    weight = id >= 0 ? 1.0f / (1.0f + expf(-v)) : 0.0f;
+    // 1 / (1 + e^-v), for v < 0 as e^v / (1 + e^v): e^-v would overflow from 88.73 on. Normalised, the
+    // factor e^-t of a negative greatest logit t cancels, so e^(v - t) / (1 + e^v) keeps the ratios
+    // of scores that are themselves below float32's normal range.
+    const float t = renorm ? fminf(value_of(top), 0.0f) : 0.0f;
+    const float s = (v < 0.0f ? expf(v - t) : 1.0f) / (1.0f + expf(-fabsf(v)));
+    weight = id >= 0 && t >= kLeastSigmoid ? s : 0.0f;
     if (renorm) {
       const float sum = wave_sum(weight);
       weight = sum > 0.0f ? weight / sum : 0.0f;

@@ -318,6 +318,36 @@ def test_route_masked_and_extreme_rows():
             assert np.array_equal(host(plan), lo.plan(want, E))
 
 
+def test_route_sigmoid_weights_of_very_negative_logits():
+    """Normalised sigmoid weights go by the ratios of the scores, also where e^-l is past float32's
+    range (l < -88.7); they are 0 only where the greatest chosen score itself is 0 in float32 (l below
+    -150 ln 2 = -103.97). The tolerance is check_weights', whose argument below 100 covers the
+    differences of logits that give a normal weight (87.3)."""
+    inf, k = np.inf, 4
+    rows = [[-88.0, -89.0, -90.0], [-89.0, -89.5], [-100.0, -101.0, -103.0, -103.9],
+            [-103.9] * 6, [-103.97, -104.5, -150.0, -300.0], [-103.98, -103.99],
+            [-103.97208], [-103.972084], [-200.0] * 4,
+            [-20.0, -88.8, -95.0, -107.0], [-17.0, -16.0, -18.5, -17.5], [5.0, -50.0, -87.0, -100.0],
+            [0.0, -80.0, -87.0], [-0.5, -88.0, -87.5], [inf, -88.0, -90.0], [-inf], [-95.0],
+            [40.0, 20.0, -60.0], [-30.0, -30.0, -118.0]]
+    for E in (8, 70, 130):
+        logits = np.full((len(rows), E), -inf, np.float32)
+        for t, r in enumerate(rows):
+            logits[t, E - len(r):] = r
+        want, _ = lo.route(logits, k, "sigmoid", False)
+        z = np.take_along_axis(logits.astype(np.float64), np.maximum(want, 0), 1)
+        s = np.where(want >= 0, 1.0 / (1.0 + np.exp(-z)), 0.0)
+        top = s[:, 0].astype(np.float32)               # correctly rounded: 0 below 2^-150
+        total = np.where(top > 0, s.sum(1), 1.0)
+        w = np.where(top[:, None] > 0, s / total[:, None], 0.0)
+        say("route: very negative logits", E)
+        ids, got, _ = gpu_route(logits, k, "sigmoid", True, True)
+        assert np.array_equal(host(ids), want)
+        check_weights(host(got), w)
+        _, got, _ = gpu_route(logits, k, "sigmoid", False, False)
+        check_weights(host(got), s)
+
+
 def test_route_many_tokens():
     M, E, k = 4099, 96, 6
     logits = np.random.default_rng(3).standard_normal((M, E)).astype(np.float32)
