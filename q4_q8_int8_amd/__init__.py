@@ -219,10 +219,19 @@ def _opts(force_tile: int = MMQ_TILE_AUTO, lds_budget: int = 0, min_workgroups: 
 
 
 @functools.lru_cache(maxsize=1024)
+def _sized_ints(fn, *args) -> int:
+    return fn(*args)
+
+
 def _sized(fn, *args) -> int:
     """fn(*args) of a size query (host arithmetic on its arguments alone): the wrappers below ask
-    for the same few sizes on every call."""
-    return fn(*args)
+    for the same few sizes on every call. Only plain ints are remembered: what else passes for an
+    integer (a 0-d tensor or array) can change, and a buffer must not be checked against a size that
+    it had before."""
+    for a in args:
+        if type(a) is not int:
+            return fn(*args)
+    return _sized_ints(fn, *args)
 
 
 def _workspace(workspace):

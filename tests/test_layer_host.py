@@ -7,7 +7,9 @@ import os
 import shutil
 import tempfile
 
+import numpy as np
 import pytest
+import torch
 
 mmq = pytest.importorskip("q4_q8_int8_amd")
 m0 = importlib.import_module("tests.test_m0_reservation")
@@ -251,3 +253,18 @@ def test_compiler_leaves_m0_to_the_loads_in_the_experts_products():
         assert not m0.compiler_m0_uses(path)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)
+
+
+@pytest.mark.parametrize("M", [np.array(4), np.int64(4), torch.tensor(4), True, 4])
+def test_sizes_of_integers_of_any_kind(M):
+    """Whatever a size query takes as an integer, the wrappers take too."""
+    assert mmq._sized(mmq.mmq_q8_1_bytes, M, 256) == mmq.mmq_q8_1_bytes(int(M), 256)
+
+
+def test_sizes_follow_an_integer_that_changes():
+    """A 0-d tensor or array that is changed in place: the buffers are checked against its value of
+    the call, not of an earlier one."""
+    for M in (torch.tensor(4), np.array(4)):
+        assert mmq._sized(mmq.mmq_q8_1_bytes, M, 256) == mmq.mmq_q8_1_bytes(4, 256)
+        M += 396
+        assert mmq._sized(mmq.mmq_q8_1_bytes, M, 256) == mmq.mmq_q8_1_bytes(400, 256)
