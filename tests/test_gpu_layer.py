@@ -2,6 +2,8 @@
 plan, the experts' products and the whole layer, against the float64 oracle and, where the
 arithmetic is the same, bit for bit against the plain product followed by float32 torch operations.
 """
+import functools
+
 import numpy as np
 import pytest
 
@@ -476,6 +478,57 @@ class ExpertsDown:
         self.E, self.D, self.F = E, D, F
         self.down = np.stack([lu.weights(D, F, seed + e) for e in range(E)])
         self.w_out = torch.cat([gpu_repack(self.down[e], D, F) for e in range(E)])
+
+
+# ---------------------------------------------------------------- more than one step of K a wavefront
+
+# every form of the down product, its wavefronts walking 2 to 17 steps of their part of K, with an odd
+# number of super-blocks (so that the last step is partly empty) and with several groups of columns
+DOWN_STEPS = [(1, 8, 2, 512, 4352),     # vector ALU, 8 rows, one token: 5 steps in 4 parts
+              (1, 16, 16, 72, 2304),    # ... 3 steps, one part
+              (1, 6, 3, 2064, 4352),    # 16 rows, one token: 9 steps in 4 parts
+              (4, 12, 2, 512, 4352),    # 8 rows, groups of 3 columns: 5 steps in 2 parts
+              (8, 8, 2, 512, 4352),     # matrix unit, 8 rows, groups of 8: 9 steps in 2 parts
+              (12, 16, 2, 40, 4352),    # 8 rows, groups of 3: 5 steps, one part, 16 experts
+              (8, 8, 2, 2064, 4352),    # vector ALU, 16 rows, groups of 4: 9 steps in 2 parts
+              (16, 3, 3, 2064, 2304),   # matrix unit, 16 rows, groups of 16: 9 steps in 4 parts
+              (20, 2, 2, 2050, 4352)]   # ... 17 steps in 8 parts, an expert of 20 columns
+
+
+@functools.lru_cache(maxsize=1)
+def down_experts(E, D, F):
+    return ExpertsDown(E, D, F)
+
+
+@pytest.mark.parametrize("M,E,k,D,F", DOWN_STEPS)
+@pytest.mark.parametrize("kind", ["distinct", "one", "padded"])
+def test_moe_down_over_several_steps(M, E, k, D, F, kind):
+    ex = down_experts(E, D, F)
+    H = synth.activations("swiglu", M * k, F, 90 + M)
+    ids = ids_of(kind, M, E, k)
+    rng = np.random.default_rng(M + F)
+    wts, res = rng.random((M, k)).astype(np.float32), rng.standard_normal((M, D)).astype(np.float32)
+    say("moe down, several steps", (M, E, k, D, F), kind)
+    got = host(gpu_down(ex, H, ids, wts, to_dev(res)))
+    lu.assert_close(got, *lu.experts_down(H, ids, wts, ex.down, res))
+
+
+# the gated product: one token (4 wavefronts over 9 or 5 steps; a token that names an expert three
+# times walks K again for each), and the matrix unit with more than 16 columns (5 steps, 2 wavefronts)
+GATED_STEPS = [(1, 8, 2, 4352, 40), (1, 4, 3, 2304, 33), (17, 2, 2, 1280, 40), (5, 8, 2, 2304, 24)]
+
+
+@pytest.mark.parametrize("M,E,k,D,F", GATED_STEPS)
+@pytest.mark.parametrize("kind", ["distinct", "repeated", "one", "padded"])
+def test_moe_gated_over_several_steps(M, E, k, D, F, kind):
+    ex = Experts(E, D, F)
+    x, ids = synth.activations("normal_outliers", M, D, 95 + M), ids_of(kind, M, E, k)
+    say("moe gated, several steps", (M, E, k, D, F), kind)
+    got = host(gpu_gated(ex, x, ids))
+    want, err = lu.experts_gated(x, ids, ex.gate, ex.up, "silu")
+    none = np.isnan(want).all(axis=1)
+    assert np.all(np.isnan(got[none])), "a row without an expert was written"
+    lu.assert_close(got[~none], want[~none], err[~none])
 
 
 def test_many_experts():
