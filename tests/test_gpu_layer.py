@@ -736,3 +736,15 @@ def test_python_checks_tensors():
     with pytest.raises(mmq.MMQArgumentError):
         mmq.mmq_q4K_moe_down(2, 8, 2, 16, 256, f32(4, 256), torch.zeros(23, dtype=torch.int32,
                              device="cuda"), f32(2, 2), raw(8 * 4608), f32(2, 16), raw(1 << 16))
+
+
+def test_current_device_and_stream_are_torch_s():
+    """The binding asks torch's C module for the device and the stream: the same as torch.cuda's."""
+    assert mmq._here() == torch.cuda.current_device()
+    streams = [torch.cuda.default_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        with torch.cuda.stream(s):
+            assert mmq._stream(None) == torch.cuda.current_stream().cuda_stream == s.cuda_stream
+            assert mmq._stream(None, mmq._here()) == s.cuda_stream
+            assert mmq._stream(s) == s.cuda_stream
+    assert mmq._stream(None) == torch.cuda.current_stream().cuda_stream
