@@ -268,3 +268,36 @@ def test_sizes_follow_an_integer_that_changes():
         assert mmq._sized(mmq.mmq_q8_1_bytes, M, 256) == mmq.mmq_q8_1_bytes(4, 256)
         M += 396
         assert mmq._sized(mmq.mmq_q8_1_bytes, M, 256) == mmq.mmq_q8_1_bytes(400, 256)
+
+
+@pytest.mark.parametrize("fn,args", [
+    ("quantize_q8_1", "x M 256 q8"), ("mmq_q4K_q8_1", "M 64 256 q8 w C"),
+    ("mmq_q6K_q8_1", "M 64 256 q8 w C"), ("mmq_q4K_f32", "M 64 256 x w C"),
+    ("mmq_q4K_q8_1_gated", "M 64 256 q8 w H"), ("mmq_q4K_f32_gated", "M 64 256 x w H"),
+    ("mmq_moe_route", "M 8 2 logits ids weights"),
+    ("mmq_q4K_moe_gated", "M 8 2 64 256 x plan w H q8"),
+    ("mmq_q4K_moe_down", "M 8 2 64 256 H plan weights w out q8"),
+    ("mmq_q4K_moe", "M 8 2 256 256 x logits w w out ws")])
+def test_calls_check_buffers_against_the_size_of_the_call(fn, args, monkeypatch):
+    """The first buffer of each call is checked for the number of tokens M that the call is given: an
+    int, a 0-d array, and a 0-d tensor that is changed in place."""
+    class Seen(Exception):
+        pass
+
+    def first(t, name, nbytes, *a, **kw):
+        raise Seen(nbytes)
+
+    monkeypatch.setattr(mmq, "_dev", first)
+
+    def size(M):
+        with pytest.raises(Seen) as e:
+            getattr(mmq, fn)(*(M if a == "M" else int(a) if a.isdigit() else a
+                               for a in args.split()))
+        return e.value.args[0]
+
+    assert size(40) > size(4) > 0
+    assert size(np.array(40)) == size(np.int32(40)) == size(40)
+    M = torch.tensor(4)
+    assert size(M) == size(4)
+    M *= 10
+    assert size(M) == size(40)
