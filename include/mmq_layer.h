@@ -51,7 +51,7 @@ typedef struct mmq_epilogue {
  * or an empty one is mmq_q4K_q8_1_ex, bit for bit; otherwise P is, bit for bit, what that call
  * computes with the same tile and splits (mmq_last_kernel reports them; with a workspace the guard
  * counts the second kernel of a split as well, so that it may leave K whole where the plain
- * product's splits it). Same limits, options and errors; MMQ_E_ARG for a bad epilogue (an act that
+ * product's, which mmq_plan answers for, splits it). Same limits, options and errors; MMQ_E_ARG for a bad epilogue (an act that
  * is none, a misaligned bias or residual, reserved != 0). bias and residual may not overlap C,
  * except a residual that is C.
  */
@@ -90,8 +90,8 @@ int mmq_gated_workspace_bytes(int64_t M, int64_t F, int64_t K, size_t* bytes);
  * mmq_q4K_q8_1_gated: q8 from quantize_q8_1 (M x K), w_pair from repack_q4_K_pair (F, K); H
  * overwritten. Each of the two sums is what mmq_q4K_q8_1_ex computes for the packed matrix of
  * 32 * ceil(F/16) rows, whose kernels, options and limits these are (mmq_last_kernel reports that
- * product; the guard's choice is mmq_q4K_q8_1_epilogue's). MMQ_ACT_NONE gives the bilinear form. mmq_q4K_f32_gated: few tokens
- * (M <= 128) from float32 activations, as mmq_q4K_f32.
+ * product; the guard's choice is mmq_q4K_q8_1_epilogue's). MMQ_ACT_NONE gives the bilinear form.
+ * mmq_q4K_f32_gated: few tokens (M <= 128) from float32 activations, as mmq_q4K_f32.
  */
 int mmq_q4K_q8_1_gated(int64_t M, int64_t F, int64_t K, const void* q8, const void* w_pair,
                        float* H, void* stream, int32_t act, const mmq_options* opt);
@@ -148,7 +148,7 @@ int mmq_moe_route(int64_t M, int64_t E, int64_t k, const float* logits, int32_t 
  * the plan with an expert e; rows of H of pairs without one are left as they were. x float32
  * [M][D]; w_pairs: E repacked pairs (F, D) one behind the other; q8: scratch of
  * mmq_q8_1_bytes(M, D) bytes (not written for one token, whose values the product quantizes
- * itself). Each used expert's weights are read once for up to 16 of its pairs.
+ * itself). A used expert's weights are read once per 16 of its pairs (for one token: once per pair).
  * M <= 64, M*k <= 512, E <= 512, D % 256 == 0, D <= 2^24, min(E, M*k) * ceil(F/16) < 2^23.
  * Errors: MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP.
  */
@@ -161,7 +161,10 @@ int mmq_q4K_moe_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, con
  * over the plan's pairs p = t*k + s; slots without an expert add nothing, and a token without any
  * gets its residual (0 if residual is NULL). H float32 [M*k][F] (rows of pairs without an expert
  * are not used); weights float32 [M][k]; w_down: E repacked q4_K matrices (D, F) one behind the
- * other; q8: scratch of mmq_q8_1_bytes(M*k, F) bytes, as above; residual may be out itself.
+ * other; q8: scratch of mmq_q8_1_bytes(M*k, F) bytes, as above; residual may be out itself. A used
+ * expert's weights are read once per 3 to 16 of its pairs (one token: per pair), the number chosen
+ * from M, E, k and D as if the experts were named evenly: a call whose tokens agree on one expert of
+ * many takes up to 2.2 times as long as one whose tokens do not.
  * M <= 64, M*k <= 512, E <= 512, F % 256 == 0, F <= 2^24, M*k*F < 2^31, D <= 2^25. Errors as
  * mmq_q4K_moe_gated.
  */

@@ -50,10 +50,13 @@ ACTIVATIONS = {"none": MMQ_ACT_NONE, "relu": MMQ_ACT_RELU, "silu": MMQ_ACT_SILU,
 MMQ_SCORE_SOFTMAX, MMQ_SCORE_SIGMOID = range(2)
 SCORES = {"softmax": MMQ_SCORE_SOFTMAX, "sigmoid": MMQ_SCORE_SIGMOID}
 MOE_MAX_TOKENS, MOE_MAX_PAIRS, MOE_MAX_EXPERTS, MOE_MAX_SLOTS = 64, 512, 512, 64
-# up to this many tokens the products from float32 activations (mmq_q4K_f32 and its forms) are the
-# better choice at most sizes: one launch, 1 token 1.5 to 2 us faster than quantize_q8_1 and the
-# product at 4096 to 22016 rows; 2 tokens 6.0 against 7.5 us at 4096 x 4096 and 18.3 against 16.1 at
-# 22016 x 4096; 3 and more only at 4096 x 4096 or below
+# The tokens up to which a program that does not look at the rows takes the products from float32
+# activations (mmq_q4K_f32 and its forms: one launch, but every row block quantizes again) before
+# quantize_q8_1 and the product. K = 4096, epilogue and gated alike (a gated product has 2 F rows): 1
+# token is 1.6 to 2.1 us faster at 2048 to 22016 rows. 2 tokens are faster to 8192 rows (4096: 5.8
+# against 7.3 us, 8192: 8.5 against 9.4) and slower above (11008: 11.4 against 10.6, 22016: 18.3 against
+# 16.2), so a program with more rows does well to take them for 1 token only. 3 and 4 tokens are
+# faster to 4096 rows (3: 6.9 against 8.0) and slower from 6144 (12.2 against 9.6).
 FUSED_TOKENS = 2
 
 

@@ -1,5 +1,5 @@
 // The two products of a mixture-of-experts layer for a few tokens, over q4_K weights and q8_1
-// activations, each reading every used expert's weights once.
+// activations, each reading a used expert's weights once per group of its columns.
 //
 // With p = t * k + s the pair (token t, slot s), e(p) its expert:
 //   gated   H[p] = act(x[t] Wg(e)^T) * (x[t] Wu(e)^T)        (pair records, epilogue.h)
@@ -9,11 +9,19 @@
 //
 // Both are bound by reading the used experts' weights (4.5 bits each; nothing else is of their
 // size): 16 tokens, 2 of 8 experts (D = 4096, F = 11008, 8 experts used) read their 406 MB of gate and
-// up weights in 83 to 95 us, 4.3 to 4.9 TB/s, a large device copy moving 5.2. A wavefront's product
-// is a DotWave (moe_dot.h, a few columns) or a MfmaWave (moe_mfma.h, up to 16), chosen on the host
-// from the columns an expert has on average. An expert with more columns than the form takes is
-// worked through in groups, its weights coming from the cache after the first. Sums are float32 in a
-// fixed order: no atomics, the same bits on every call.
+// up weights in 89 us, 4.5 TB/s (graph replays over six copies, quantization included), a large device
+// copy moving 5.2. A wavefront's product is a DotWave (moe_dot.h, a few columns) or a MfmaWave
+// (moe_mfma.h, up to 16). An expert with more columns than the form takes (gated: 16, with one token 1;
+// down: 16, 8, 4, 3 or 1) is worked through in groups, its weights read again for each, in part from
+// the caches (the gated product of 64 tokens, 2 of 8, reads 613 MB for 406 MB of weights). Sums are
+// float32 in a fixed order: no atomics, the same bits on every call.
+//
+// The host does not know the plan, so it chooses the form from the columns an expert would have if the
+// experts were chosen evenly, and the down product gives a wavefront whole experts (or a part of K by
+// the number that could be used at most). Where the tokens agree on few experts both are off: 64
+// tokens of one slot all to one of 64 experts (F = 1024) take 34.8 us gated and 40.2 down at D = 2048,
+// 60.3 and 50.4 at D = 4096, against 27.5 and 18.3, 49.1 and 24.5 where they name 37 experts, most
+// of the wavefronts of the down product having nothing to do.
 #include <cmath>
 
 #include "epilogue.h"
@@ -341,9 +349,10 @@ auto with_down(const MoeShape& m, int64_t compute_units, F f) {
   // against 14.7 us, at 1.5 (8 tokens) 16.8 against 19.3, at 2.4 (23 tokens, 6 of 64, F = 1280) 30.9
   // against 30.6 (29.5 against 24.9 while the weights fit the cache), at 8 (64 tokens) 52.7 against
   // 44.0. D = 4096: at 1.5 (4 tokens, 2 of 8, F = 11008) 33.8 against 47.4, at 3.1 (12 tokens, 4 of
-  // 16, F = 4096) 41.7 against 43.1, at 4 (16 tokens, 2 of 8) 57.8 against 59.9, at 16 (64 tokens) 168
-  // against 101. Its step is twice the matrix unit's bytes per wavefront, which counts while loads
-  // in flight set the rate.
+  // 16, F = 4096) 40.3 against 41.9, at 4 (16 tokens, 2 of 8) 57.9 against 58.2, but 58.2 against 43.1
+  // for 16 tokens, 4 of 16, whose most liked expert has 13 columns, four groups of 4; at 16 (64 tokens)
+  // 183 against 103. Its step is twice the matrix unit's bytes per wavefront, which counts while
+  // loads in flight set the rate.
   if (narrow)
     return c <= 2.0 ? f(Form<DotWave<8, 3, false>, 16>{})
                     : f(Form<MfmaWave<1, 2>, 16>{});
@@ -362,7 +371,10 @@ hipError_t launch_moe_gated(const void* tokens, const int* plan, const void* w, 
   // half of K: the prologue and the sum over wavefronts weigh less (4 and 8 tokens were slower by
   // up to 8 %), while one per workgroup leaves the short K of small experts unsplit.
   if (moe_fused(m.M)) return launch_gated<DotWave<16, 1, true>, 4>(tokens, plan, w, H, m, act, s);
-  // above 8 columns on average some experts have more than 16: their weights are read again
+  // Above 8 columns on average some experts have more than 16: their weights are read again. Loaded as
+  // read once against not, D = 4096: 8 columns (64 tokens, 8 of 64, F = 1024) 82.2 / 85.8 us, 9 (36
+  // tokens, 2 of 8, F = 11008) 108.2 / 110.7, 12 (48) 112.8 / 114.7, 16 (64) 149.7 / 142.4: the two
+  // sides meet between 12 and 16, and the switch at 8 costs 2 % between.
   return columns_per_expert(m) <= 8.0
              ? launch_gated<MfmaWave<2, 1, true>, 2>(tokens, plan, w, H, m, act, s)
              : launch_gated<MfmaWave<2>, 2>(tokens, plan, w, H, m, act, s);

@@ -122,9 +122,12 @@ struct DotWave {
   }
 
   // The parts of a step's loads: step j, rows j0 .. of the tile of `rw`, columns of g. With 16 rows
-  // the nibbles are loaded as read once (the down product of 4 tokens, 2 of 8 experts of 4096 x
-  // 11008: 36.7 -> 34.6 us; with 8 rows, whose outputs are small, it made no difference beyond the
-  // cache, 31.0 and 30.7 us for 23 tokens, 6 of 64, and cost 5 us of 25 while they fit it).
+  // the nibbles are loaded as read once, although an expert of more columns than MT reads them again:
+  // the down product of 2 of 8 experts of 4096 x 11008 takes 31.6 us so against 35.2 for 4 tokens, 57.9
+  // against 60.7 for 16 (4 columns on average); at 5 columns the two are equal (16 tokens, 4 of 16:
+  // 58.2, 58.3), and above this form is not chosen. With 8 rows, whose outputs are small, it made no
+  // difference beyond the cache, 31.0 and 30.7 us for 23 tokens, 6 of 64, and cost 5 us of 25 while
+  // they fit it.
   static constexpr int kAux = RW == 16 ? kReadOnce : 0;
   struct Src {
     __amdgpu_buffer_rsrc_t rw;

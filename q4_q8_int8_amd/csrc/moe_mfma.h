@@ -16,7 +16,7 @@
 //
 // Up to 16 columns cost what one does, 165 vector instructions per super-block and 16 rows, 64 of
 // them the rescale. That bounds the form beside the memory: at 16 tokens, 2 of 8 experts (D = 4096, F =
-// 11008) the vector ALU is 67 % busy while the weights come at 4.3 to 4.9 TB/s.
+// 11008) the vector ALU is 63 % busy while the weights come at 4.5 TB/s.
 //
 // KS = 2: 8 weight rows and two super-blocks at a time. Operand rows 0..7 are the rows of the first
 // super-block and 8..15 the same rows of the second, operand columns 0..7 the columns of the first
@@ -36,8 +36,8 @@ namespace mmq {
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 // ONCE: the weights are read once (an expert has no second group of columns, as a rule), and loaded
-// so: 16 tokens, 2 of 8 experts, the gated product 101 -> 95 us; 64 tokens, with experts of more than 16
-// columns, 142 -> 150.
+// so: 16 tokens, 2 of 8 experts, the gated product 96.5 -> 90.2 us; 64 tokens, with experts of more than
+// 16 columns, 142 -> 150.
 template <int RT, int KS = 1, bool ONCE = false>
 struct MfmaWave {
   static_assert(KS == 1 || (KS == 2 && RT == 1), "forms");
