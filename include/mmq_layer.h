@@ -51,9 +51,9 @@ typedef struct mmq_epilogue {
  * or an empty one is mmq_q4K_q8_1_ex, bit for bit; otherwise P is, bit for bit, what that call
  * computes with the same tile and splits (mmq_last_kernel reports them; with a workspace the guard
  * counts the second kernel of a split as well, so that it may leave K whole where the plain
- * product's, which mmq_plan answers for, splits it). Same limits, options and errors; MMQ_E_ARG for a bad epilogue (an act that
- * is none, a misaligned bias or residual, reserved != 0). bias and residual may not overlap C,
- * except a residual that is C.
+ * product's, which mmq_plan answers for, splits it). Same limits, options and errors; MMQ_E_ARG for a
+ * bad epilogue (an act that is none, a misaligned bias or residual, reserved != 0). bias and residual
+ * may not overlap C, except a residual that is C.
  */
 int mmq_q4K_q8_1_epilogue(int64_t M, int64_t N, int64_t K, const void* q8, const void* w_rep,
                           float* C, void* stream, const mmq_epilogue* epi,
