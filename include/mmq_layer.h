@@ -1,7 +1,7 @@
 /*
  * mmq_layer.h -- C ABI of the layer operators of libmmq.so, beside the q4_K x q8_1 product of
- * mmq.h: the product with an epilogue, its gated two-matrix form, and a mixture-of-experts layer
- * for a few tokens with its router.
+ * mmq.h: the product with an epilogue, its gated two-matrix form, a mixture-of-experts layer for a
+ * few tokens with its router, and the layer's products grouped by expert for any number of tokens.
  *
  * P below is the product of mmq.h, P_ij = sum_b (da_ib dsv_jb S_ijb + dmv_jb da_ib sa_ib), over
  * activations quantized to q8_1 and q4_K weights; everything after it is float32.
@@ -182,6 +182,81 @@ int mmq_q4K_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const flo
                 const float* logits, int32_t score, int32_t renorm, const void* w_pairs,
                 int32_t act, const void* w_down, const float* residual, float* out,
                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------- products grouped by expert */
+
+/*
+ * The mixture-of-experts layer for more tokens than a plan takes, and for any raggedness: the
+ * (token, slot) pairs p = t*k + s are sorted by expert on the device, and one launch runs each
+ * expert's rows, however many, against its matrix. Nothing about the counts has to be known on the
+ * host. Per pair the products are, bit for bit, what mmq_q4K_q8_1_ex computes for its row and its
+ * expert's matrix with MMQ_TILE_LARGE (or HALF, MEDIUM, SMALL) and one split.
+ *
+ * Limits of all of them: 1 <= M*k <= 2^21, E <= 512, k <= min(E, 64).
+ */
+#define MMQ_GROUP_MAX_PAIRS (1 << 21)
+
+/*
+ * mmq_moe_group: the groups of ids (int32 [M][k], the expert of each pair, from mmq_moe_route or
+ * elsewhere; an id outside [0, E) names no expert: a padded token, an expert of another device).
+ * groups, int32, mmq_moe_group_bytes(M, E, k) bytes, each part starting at a multiple of 4 words:
+ *   offsets[E + 1]  the pairs of expert e are order[offsets[e] .. offsets[e + 1])
+ *   order[M*k]      the pairs sorted by expert, those of one expert in increasing order, those without
+ *                   one replaced by -1 at the end
+ *   place[M*k]      where each pair is in order, -1 without an expert
+ * and behind them words of its own (unspecified). The products bound-check what they read of the
+ * groups; groups made for other M, E, k give unspecified results.
+ */
+int mmq_moe_group_bytes(int64_t M, int64_t E, int64_t k, size_t* bytes);
+int mmq_moe_group(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* groups,
+                  void* stream);
+
+/*
+ * mmq_q4K_grouped: C[p][N] = act(x[r] W(e)^T) for every pair p with an expert e; rows of C of pairs
+ * without one are left as they were. per_pair = 0: x float32 [M][K], a row per token, r = p / k;
+ * per_pair = 1: x [M*k][K], a row per pair, r = p. w_rep: E repacked q4_K matrices (N, K) one behind
+ * the other; q8: scratch of mmq_q8_1_bytes(rows of x, K) bytes (in a layout of its own).
+ * mmq_q4K_grouped_gated: H[p][F] = act(x[p / k] Wg(e)^T) * (x[p / k] Wu(e)^T), x float32 [M][D],
+ * w_pairs: E repacked pairs (F, D); q8: scratch of mmq_q8_1_bytes(M, D) bytes. For at most 64 tokens
+ * mmq_q4K_moe_gated computes the same with a plan; it is the faster one there.
+ * K % 256 == 0, K <= 2^24, (rows of x)*K < 2^31, N <= 2^30, and (M*k/32 + min(E, M*k)) * ceil(N/256)
+ * < 2^23 (gated: of its 32 * ceil(F/16) packed rows).
+ * Errors: MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP.
+ */
+int mmq_q4K_grouped(int64_t M, int64_t E, int64_t k, int64_t N, int64_t K, const float* x,
+                    int32_t per_pair, const int32_t* groups, const void* w_rep, float* C, void* q8,
+                    int32_t act, void* stream);
+int mmq_q4K_grouped_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, const float* x,
+                          const int32_t* groups, const void* w_pairs, float* H, void* q8,
+                          int32_t act, void* stream);
+
+/*
+ * mmq_q4K_grouped_down: out[t][D] = residual[t] + sum over the slots s of weights[t][s] * (H[p]
+ * W(e)^T) over the pairs p = t*k + s with an expert, in float32 and in the order of the slots; a token
+ * without any gets its residual (0 if residual is NULL). H float32 [M*k][F] (rows of pairs without
+ * an expert may hold anything: they are read, not used); weights float32 [M][k]; w_down: E repacked
+ * q4_K matrices (D, F); residual may be out itself. workspace:
+ * mmq_grouped_down_workspace_bytes(M, E, k, D, F) bytes, for H in q8_1 and the pairs' products.
+ * Limits as mmq_q4K_grouped with N = D, K = F and M*k rows; M * ceil(D/256) < 2^24.
+ */
+int mmq_grouped_down_workspace_bytes(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F,
+                                     size_t* bytes);
+int mmq_q4K_grouped_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const float* H,
+                         const int32_t* groups, const float* weights, const void* w_down,
+                         const float* residual, float* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * mmq_q4K_grouped_moe: the whole layer: mmq_moe_route on the router's logits [M][E], mmq_moe_group,
+ * mmq_q4K_grouped_gated and mmq_q4K_grouped_down, bit for bit what those calls give one after the
+ * other. workspace: mmq_grouped_moe_workspace_bytes(M, E, k, D, F) bytes (D, F multiples of 256).
+ */
+int mmq_grouped_moe_workspace_bytes(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F,
+                                    size_t* bytes);
+int mmq_q4K_grouped_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const float* x,
+                        const float* logits, int32_t score, int32_t renorm, const void* w_pairs,
+                        int32_t act, const void* w_down, const float* residual, float* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

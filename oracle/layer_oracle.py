@@ -123,3 +123,18 @@ def plan(ids, E: int):
     head = [used, len(order), 0, 0]
     order += [-1] * (P - len(order))
     return np.array(head + [v for r in rows for v in r] + order, np.int32)
+
+
+def groups(ids, E: int):
+    """(offsets [E + 1], order, place) of ids [M, k], int32: where each expert's pairs begin, the pairs
+    sorted by expert (those without one -1, at the end), and the place of each."""
+    flat = np.asarray(ids).reshape(-1)
+    P = flat.size
+    offsets, order = [0], []
+    for e in range(E):
+        order += np.nonzero(flat == e)[0].tolist()
+        offsets.append(len(order))
+    place = np.full(P, -1, np.int32)
+    place[order] = np.arange(len(order))
+    order += [-1] * (P - len(order))
+    return np.array(offsets, np.int32), np.array(order, np.int32), place

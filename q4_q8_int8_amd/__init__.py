@@ -1,8 +1,9 @@
 """q4_K x q8_1 quantized matrix multiply (MMQ) on MI355X (gfx950).
 
 A thin ctypes binding over libmmq.so, whose C ABI is declared in include/mmq.h (the integer
-product), include/mmq_layer.h (its epilogue, the gated product, the mixture-of-experts layer) and
-include/mmq_f16.h (the f16 comparator path). The functions here have the same
+product), include/mmq_layer.h (its epilogue, the gated product, the mixture-of-experts layer),
+include/mmq_q4g.h (matrix-vector products with group scales) and include/mmq_f16.h (the f16
+comparator path). The functions here have the same
 names and arguments as the C entry points and only marshal arguments: each tensor is checked
 (a contiguous CUDA tensor on the current device, of the expected dtype and at least the size
 the call reads or writes; MMQArgumentError otherwise) and passed as a device pointer, the
@@ -23,7 +24,7 @@ LIB_PATH = os.path.join(_PKG, "libmmq.so")
 INCLUDE_DIR = os.path.join(os.path.dirname(_PKG), "include")
 HEADER_PATH = os.path.join(INCLUDE_DIR, "mmq.h")
 HEADER_PATHS = (HEADER_PATH, os.path.join(INCLUDE_DIR, "mmq_layer.h"),
-                os.path.join(INCLUDE_DIR, "mmq_f16.h"))
+                os.path.join(INCLUDE_DIR, "mmq_q4g.h"), os.path.join(INCLUDE_DIR, "mmq_f16.h"))
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python q4_q8_int8_amd/build.py`")
@@ -50,6 +51,10 @@ ACTIVATIONS = {"none": MMQ_ACT_NONE, "relu": MMQ_ACT_RELU, "silu": MMQ_ACT_SILU,
 MMQ_SCORE_SOFTMAX, MMQ_SCORE_SIGMOID = range(2)
 SCORES = {"softmax": MMQ_SCORE_SOFTMAX, "sigmoid": MMQ_SCORE_SIGMOID}
 MOE_MAX_TOKENS, MOE_MAX_PAIRS, MOE_MAX_EXPERTS, MOE_MAX_SLOTS = 64, 512, 512, 64
+GROUP_MAX_PAIRS = 1 << 21
+MMQ_F32, MMQ_F16, MMQ_BF16 = range(3)
+TYPES = {torch.float32: MMQ_F32, torch.float16: MMQ_F16, torch.bfloat16: MMQ_BF16}
+Q4G_MAX_TOKENS = 16
 # The tokens up to which a program that does not look at the rows takes the products from float32
 # activations (mmq_q4K_f32 and its forms: one launch, but every row block quantizes again) before
 # quantize_q8_1 and the product. K = 4096, epilogue and gated alike (a gated product has 2 F rows): 1
@@ -80,6 +85,16 @@ class mmq_kernel_info(ctypes.Structure):
 
 
 class mmq_epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class mmq_q4G_format(ctypes.Structure):
+    _fields_ = [("group", ctypes.c_int32), ("scale_type", ctypes.c_int32),
+                ("zeros", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class mmq_q4G_epilogue(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
                 ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
@@ -134,6 +149,20 @@ _SIGS = {
     "mmq_moe_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)],
     "mmq_q4K_moe": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _i32c, _i32c, _vp, _i32c, _vp, _vp,
                     _vp, _vp, _sz, _vp],
+    "mmq_moe_group_bytes": [_i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_moe_group": [_i64, _i64, _i64, _vp, _vp, _vp],
+    "mmq_q4K_grouped": [_i64, _i64, _i64, _i64, _i64, _vp, _i32c, _vp, _vp, _vp, _vp, _i32c, _vp],
+    "mmq_q4K_grouped_gated": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32c, _vp],
+    "mmq_grouped_down_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_q4K_grouped_down": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                             _vp],
+    "mmq_grouped_moe_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, ctypes.POINTER(_sz)],
+    "mmq_q4K_grouped_moe": [_i64, _i64, _i64, _i64, _i64, _vp, _vp, _i32c, _i32c, _vp, _i32c, _vp,
+                            _vp, _vp, _vp, _sz, _vp],
+    "mmq_q4G_repacked_bytes": [_i64, _i64, ctypes.POINTER(mmq_q4G_format), ctypes.POINTER(_sz)],
+    "repack_q4_G": [_vp, _vp, _vp, _i64, _i64, ctypes.POINTER(mmq_q4G_format), _vp, _vp],
+    "mmq_q4G": [_i64, _i64, _i64, _i32c, _vp, _vp, ctypes.POINTER(mmq_q4G_format), _i32c, _vp,
+                ctypes.POINTER(mmq_q4G_epilogue), _vp],
     "mmq_f16_bytes": [_i64, _i64, ctypes.POINTER(_sz)],
     "convert_f32_f16": [_vp, _i64, _i64, _vp, _vp],
     "dequantize_q4_K_f16": [_vp, _i64, _i64, _vp, _vp],
@@ -572,6 +601,214 @@ def mmq_q4K_moe(M: int, E: int, k: int, D: int, F: int, x, logits, w_pairs, w_do
     _check("mmq_q4K_moe",
            _lib.mmq_q4K_moe(M, E, k, D, F, xp, lp, score, int(renorm), gp, act, dp, rp, op, sp, sb,
                             _stream(stream, here)))
+
+
+# ---------------------------------------------------------------- products grouped by expert
+def mmq_moe_group_bytes(M: int, E: int, k: int) -> int:
+    n = _sz()
+    _check("mmq_moe_group_bytes", _lib.mmq_moe_group_bytes(M, E, k, ctypes.byref(n)))
+    return n.value
+
+
+@_sizes
+def _group_sizes(M, E, k):
+    return 4 * M * k, mmq_moe_group_bytes(M, E, k)
+
+
+def mmq_moe_group(M: int, E: int, k: int, ids, groups, stream=None) -> None:
+    """groups (int32, mmq_moe_group_bytes): the pairs of ids int32 [M, k] sorted by expert; an id
+    outside [0, E) is no expert. moe_groups gives its parts."""
+    here = _here()
+    n, gn = _group_sizes(_int(M), _int(E), _int(k))
+    ip = _dev(ids, "ids", n, torch.int32, here)
+    gp = _dev(groups, "groups", gn, torch.int32, here)
+    _check("mmq_moe_group", _lib.mmq_moe_group(M, E, k, ip, gp, _stream(stream, here)))
+
+
+def moe_groups(groups, M: int, E: int, k: int):
+    """Views (offsets [E + 1], order [M*k], place [M*k]) of what mmq_moe_group wrote."""
+    M, E, k = _int(M), _int(E), _int(k)
+    need = _group_sizes(M, E, k)[1]
+    if groups.dtype != torch.int32 or not groups.is_contiguous() or groups.nbytes < need:
+        raise MMQArgumentError(f"groups: must be a contiguous int32 tensor of {need} bytes or more")
+    P, flat = M * k, groups.flatten()
+    a = (E + 1 + 3) // 4 * 4
+    b = a + (P + 3) // 4 * 4
+    return flat[:E + 1], flat[a:a + P], flat[b:b + P]
+
+
+@_sizes
+def _grouped_sizes(M, E, k, N, K, per_pair):
+    rows = M * k if per_pair else M
+    return (4 * rows * K, mmq_moe_group_bytes(M, E, k), E * mmq_q4K_repacked_bytes(N, K),
+            4 * M * k * N, mmq_q8_1_bytes(rows, K))
+
+
+@_sizes
+def _grouped_gated_sizes(M, E, k, F, D):
+    return (4 * M * D, mmq_moe_group_bytes(M, E, k), E * mmq_q4K_pair_bytes(F, D), 4 * M * k * F,
+            mmq_q8_1_bytes(M, D))
+
+
+@_sizes
+def _grouped_down_sizes(M, E, k, D, F):
+    return (4 * M * k * F, mmq_moe_group_bytes(M, E, k), 4 * M * k,
+            E * mmq_q4K_repacked_bytes(D, F), 4 * M * D,
+            mmq_grouped_down_workspace_bytes(M, E, k, D, F))
+
+
+@_sizes
+def _grouped_moe_sizes(M, E, k, D, F):
+    return (4 * M * D, 4 * M * E, E * mmq_q4K_pair_bytes(F, D), E * mmq_q4K_repacked_bytes(D, F),
+            mmq_grouped_moe_workspace_bytes(M, E, k, D, F))
+
+
+def mmq_q4K_grouped(M: int, E: int, k: int, N: int, K: int, x, groups, w_rep, C, q8,
+                    per_pair: bool = False, act: int = MMQ_ACT_NONE, stream=None) -> None:
+    """C[M*k, N] (f32) = act(x[r] W(expert)^T) per pair p of the groups, r = p // k (x [M, K]) or, with
+    per_pair, p (x [M*k, K]). w_rep: E repacked matrices; q8: scratch, mmq_q8_1_bytes(rows of x, K)."""
+    here = _here()
+    xn, gn, wn, cn, qn = _grouped_sizes(_int(M), _int(E), _int(k), _int(N), _int(K),
+                                        bool(per_pair))
+    xp = _dev(x, "x", xn, torch.float32, here)
+    gp = _dev(groups, "groups", gn, torch.int32, here)
+    wp = _dev(w_rep, "w_rep", wn, here=here)
+    cp = _dev(C, "C", cn, torch.float32, here)
+    qp = _dev(q8, "q8", qn, here=here)
+    _check("mmq_q4K_grouped",
+           _lib.mmq_q4K_grouped(M, E, k, N, K, xp, int(bool(per_pair)), gp, wp, cp, qp, act,
+                                _stream(stream, here)))
+
+
+def mmq_q4K_grouped_gated(M: int, E: int, k: int, F: int, D: int, x, groups, w_pairs, H, q8,
+                          act: int = MMQ_ACT_SILU, stream=None) -> None:
+    """H[M*k, F] (f32): per pair of the groups the gated product of its expert, for any number of
+    tokens. w_pairs: E repacked pairs; q8: scratch, mmq_q8_1_bytes(M, D)."""
+    here = _here()
+    xn, gn, wn, hn, qn = _grouped_gated_sizes(_int(M), _int(E), _int(k), _int(F), _int(D))
+    xp = _dev(x, "x", xn, torch.float32, here)
+    gp = _dev(groups, "groups", gn, torch.int32, here)
+    wp = _dev(w_pairs, "w_pairs", wn, here=here)
+    hp = _dev(H, "H", hn, torch.float32, here)
+    qp = _dev(q8, "q8", qn, here=here)
+    _check("mmq_q4K_grouped_gated",
+           _lib.mmq_q4K_grouped_gated(M, E, k, F, D, xp, gp, wp, hp, qp, act,
+                                      _stream(stream, here)))
+
+
+def mmq_grouped_down_workspace_bytes(M: int, E: int, k: int, D: int, F: int) -> int:
+    n = _sz()
+    _check("mmq_grouped_down_workspace_bytes",
+           _lib.mmq_grouped_down_workspace_bytes(M, E, k, D, F, ctypes.byref(n)))
+    return n.value
+
+
+def mmq_q4K_grouped_down(M: int, E: int, k: int, D: int, F: int, H, groups, weights, w_down, out,
+                         workspace, residual=None, stream=None) -> None:
+    """out[M, D] (f32) = residual + per token the weighted sum over its slots of H[p] W(expert)^T.
+    workspace: mmq_grouped_down_workspace_bytes(M, E, k, D, F) bytes; residual may be out."""
+    here = _here()
+    hn, gn, tn, wn, on, sn = _grouped_down_sizes(_int(M), _int(E), _int(k), _int(D), _int(F))
+    hp = _dev(H, "H", hn, torch.float32, here)
+    gp = _dev(groups, "groups", gn, torch.int32, here)
+    tp = _dev(weights, "weights", tn, torch.float32, here)
+    wp = _dev(w_down, "w_down", wn, here=here)
+    op = _dev(out, "out", on, torch.float32, here)
+    rp = None if residual is None else _dev(residual, "residual", on, torch.float32, here)
+    sp = _dev(workspace, "workspace", sn, here=here)
+    _check("mmq_q4K_grouped_down",
+           _lib.mmq_q4K_grouped_down(M, E, k, D, F, hp, gp, tp, wp, rp, op, sp, workspace.nbytes,
+                                     _stream(stream, here)))
+
+
+def mmq_grouped_moe_workspace_bytes(M: int, E: int, k: int, D: int, F: int) -> int:
+    n = _sz()
+    _check("mmq_grouped_moe_workspace_bytes",
+           _lib.mmq_grouped_moe_workspace_bytes(M, E, k, D, F, ctypes.byref(n)))
+    return n.value
+
+
+def mmq_q4K_grouped_moe(M: int, E: int, k: int, D: int, F: int, x, logits, w_pairs, w_down, out,
+                        workspace, score: int = MMQ_SCORE_SOFTMAX, renorm: bool = True,
+                        act: int = MMQ_ACT_SILU, residual=None, stream=None) -> None:
+    """The whole layer for any number of tokens: out[M, D] = residual + experts of x [M, D] chosen by
+    the router's logits [M, E]. workspace: mmq_grouped_moe_workspace_bytes(M, E, k, D, F) bytes."""
+    here = _here()
+    xn, ln, gn, dn, sn = _grouped_moe_sizes(_int(M), _int(E), _int(k), _int(D), _int(F))
+    xp = _dev(x, "x", xn, torch.float32, here)
+    lp = _dev(logits, "logits", ln, torch.float32, here)
+    gp = _dev(w_pairs, "w_pairs", gn, here=here)
+    dp = _dev(w_down, "w_down", dn, here=here)
+    op = _dev(out, "out", xn, torch.float32, here)
+    rp = None if residual is None else _dev(residual, "residual", xn, torch.float32, here)
+    sp = _dev(workspace, "workspace", sn, here=here)
+    _check("mmq_q4K_grouped_moe",
+           _lib.mmq_q4K_grouped_moe(M, E, k, D, F, xp, lp, score, int(renorm), gp, act, dp, rp, op,
+                                    sp, workspace.nbytes, _stream(stream, here)))
+
+
+# ---------------------------------------------------------------- group scales (q4_G)
+def q4G_format(group: int, scale_dtype, zeros: bool) -> mmq_q4G_format:
+    """How the weights of a q4_G matrix are scaled: `group` values share a scale (and, with zeros, a
+    zero) of scale_dtype, torch.float16 or torch.bfloat16."""
+    if scale_dtype not in (torch.float16, torch.bfloat16):
+        raise MMQArgumentError(f"scale_dtype: must be float16 or bfloat16, got {scale_dtype}")
+    return mmq_q4G_format(_int(group), TYPES[scale_dtype], int(bool(zeros)), 0)
+
+
+@_sizes
+def _q4G_bytes(N, K, group, scale_type, zeros, reserved):
+    n = _sz()
+    _check("mmq_q4G_repacked_bytes",
+           _lib.mmq_q4G_repacked_bytes(N, K, mmq_q4G_format(group, scale_type, zeros, reserved),
+                                       ctypes.byref(n)))
+    return n.value
+
+
+def _q4G_size(N, K, f):
+    return _q4G_bytes(_int(N), _int(K), f.group, f.scale_type, f.zeros, f.reserved)
+
+
+def mmq_q4G_repacked_bytes(N: int, K: int, format: mmq_q4G_format) -> int:
+    return _q4G_size(N, K, format)
+
+
+def repack_q4_G(w, scales, zeros, N: int, K: int, format: mmq_q4G_format, w_rep,
+                stream=None) -> None:
+    """w: uint8 [N, K/2], the even value of two in the low four bits; scales and zeros (None where the
+    format has none): [N, ceil(K/group)] of the format's type; w_rep: mmq_q4G_repacked_bytes."""
+    here = _here()
+    rn = _q4G_size(N, K, format)
+    dtype = torch.float16 if format.scale_type == MMQ_F16 else torch.bfloat16
+    n = 2 * N * -(-K // format.group)
+    wp = _dev(w, "w", N * K // 2, torch.uint8, here)
+    sp = _dev(scales, "scales", n, dtype, here)
+    zp = None if zeros is None else _dev(zeros, "zeros", n, dtype, here)
+    rp = _dev(w_rep, "w_rep", rn, here=here)
+    _check("repack_q4_G", _lib.repack_q4_G(wp, sp, zp, N, K, ctypes.byref(format), rp,
+                                           _stream(stream, here)))
+
+
+def mmq_q4G(M: int, N: int, K: int, x, w_rep, format: mmq_q4G_format, y, bias=None, residual=None,
+            act: int = MMQ_ACT_NONE, stream=None) -> None:
+    """y[M, N] = act(x[M, K] W^T + bias[N]) + residual[M, N] for 1 <= M <= 16 tokens. x and y: float32,
+    float16 or bfloat16 each; residual of y's type (it may be y), bias float32."""
+    here = _here()
+    rn = _q4G_size(N, K, format)
+    xt, yt = TYPES.get(getattr(x, "dtype", None)), TYPES.get(getattr(y, "dtype", None))
+    if xt is None or yt is None:
+        raise MMQArgumentError("x and y: must be float32, float16 or bfloat16 tensors")
+    yn = M * N * (4 if yt == MMQ_F32 else 2)
+    xp = _dev(x, "x", M * K * (4 if xt == MMQ_F32 else 2), None, here)
+    rp = _dev(w_rep, "w_rep", rn, here=here)
+    yp = _dev(y, "y", yn, None, here)
+    epi = None
+    if bias is not None or residual is not None or act != MMQ_ACT_NONE:
+        epi = ctypes.byref(mmq_q4G_epilogue(
+            None if bias is None else _dev(bias, "bias", 4 * N, torch.float32, here),
+            None if residual is None else _dev(residual, "residual", yn, y.dtype, here), act, 0))
+    _check("mmq_q4G", _lib.mmq_q4G(M, N, K, xt, xp, rp, ctypes.byref(format), yt, yp, epi,
+                                   _stream(stream, here)))
 
 
 # ---------------------------------------------------------------- the q6_K variant

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libmmq.so")
 
 SOURCES = ["quantize.hip", "repack.hip", "mmq_gemm.hip", "mmq_skinny.hip", "mmq_gemv.hip",
            "f16_path.hip", "f16_gemm.hip", "static_scratch.hip", "moe.hip", "moe_route.hip",
-           "api.cpp", "moe_api.cpp"]
+           "group.hip",
+           "grouped.hip", "q4g.hip", "api.cpp", "moe_api.cpp", "grouped_api.cpp", "q4g_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -66,7 +67,7 @@ def build(verbose: bool = False) -> str:
             lang = ["-x", "hip"] if src.endswith(".hip") else []
             cmds.append([HIPCC, *FLAGS, *lang, "-c",
                          os.path.join(CSRC, src), "-o", obj])
-        with ThreadPoolExecutor(max_workers=min(4, len(cmds))) as ex:
+        with ThreadPoolExecutor(max_workers=min(8, len(cmds))) as ex:
             for cmd, _ in zip(cmds, ex.map(_run, cmds)):
                 if verbose:
                     print(" ".join(cmd))

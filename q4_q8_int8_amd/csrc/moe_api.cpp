@@ -3,11 +3,10 @@
 // argument has been checked.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <initializer_list>
 
+#include "api_util.h"
 #include "mmq.h"
 #include "mmq_internal.h"
 #include "mmq_layer.h"
@@ -15,16 +14,9 @@
 
 namespace {
 
-int fail(int status, const char* fmt, ...) {
-  char msg[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(msg, sizeof(msg), fmt, ap);
-  va_end(ap);
-  return mmq::api_fail(status, msg);
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using mmq::check_pointers;
+using mmq::fail;
+using mmq::hip_status;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 // A grid holds fewer than 2^32 work-items: the router launches 64 per token, the down product at most
@@ -65,20 +57,6 @@ int check_product(const char* rows_name, int64_t rows, const char* k_name, int64
     return fail(MMQ_E_SHAPE, "activations of %lld x %lld: 2^31 values or more", (long long)q8_rows,
                 (long long)K);
   return MMQ_OK;
-}
-
-int check_pointers(std::initializer_list<const void*> needed, const void* optional = nullptr) {
-  for (const void* p : needed) {
-    if (!p) return fail(MMQ_E_ARG, "null device pointer");
-    if (!aligned16(p)) return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");
-  }
-  if (!aligned16(optional)) return fail(MMQ_E_ARG, "device pointers must be 16-byte aligned");
-  return MMQ_OK;
-}
-
-int hip_status(const char* what, hipError_t e) {
-  return e == hipSuccess ? mmq::api_ok()
-                         : fail(MMQ_E_HIP, "%s launch: %s", what, hipGetErrorString(e));
 }
 
 // The device's compute units, and that the down product's kernel fits its LDS (the gated ones and

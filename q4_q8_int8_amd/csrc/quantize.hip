@@ -20,6 +20,7 @@
 //   16-byte store per row scattered M entries apart;
 // - any other K: each wavefront takes 2 groups of 8 consecutive blocks, 8 lanes per block,
 //   and stores every block's plane entries where they fall.
+#include "grouped_internal.h"
 #include "quant_device.h"
 
 namespace mmq {
@@ -142,6 +143,8 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
          ((uint32_t)d << 24);
 }
 
+// ROWS: the (da, nda) pairs row by row, [M][K/32], for the products that gather rows (grouped.hip).
+template <bool ROWS>
 __global__ __launch_bounds__(64 * kTileWaves) void quantize_q8_1_tiled_kernel(
     const float4* __restrict__ x, uint32_t* __restrict__ qs, uint32_t* __restrict__ ds,
     float* __restrict__ da_plane, uint16_t* __restrict__ pieces, uint32_t M, uint32_t K,
@@ -210,7 +213,15 @@ __global__ __launch_bounds__(64 * kTileWaves) void quantize_q8_1_tiled_kernel(
   __syncthreads();
   const int t = threadIdx.x;
   constexpr int kDaThreads = 4 * kTileRows;  // 8 blocks x kTileRows/2 row pairs
-  if (t < kDaThreads) {
+  if (ROWS && t < kDaThreads) {  // two blocks of a row
+    const int rr = t / 4, bp = t % 4;
+    const uint32_t r = r0 + rr;
+    if (r < M) {
+      const float2 a = sDa[2 * bp][rr], b2 = sDa[2 * bp + 1][rr];
+      *reinterpret_cast<float4*>(da_plane + 2 * ((size_t)r * (K / 32) + 8 * s + 2 * bp)) =
+          make_float4(a.x, a.y, b2.x, b2.y);
+    }
+  } else if (t < kDaThreads) {
     const int bb = t / (kTileRows / 2), cc = t % (kTileRows / 2);
     const uint32_t r = r0 + 2 * cc;
     float2* dst = reinterpret_cast<float2*>(da_plane) + (8 * s + bb) * M + r;
@@ -232,20 +243,30 @@ __global__ __launch_bounds__(64 * kTileWaves) void quantize_q8_1_tiled_kernel(
 
 }  // namespace
 
+namespace {
+template <bool ROWS>
+hipError_t launch_tiled(const float* x, int64_t M, int64_t K, void* q8, hipStream_t s) {
+  uint8_t* base = static_cast<uint8_t*>(q8);
+  // ceil(M/8) * K/256 workgroups of 256 work-items: below 2^31 work-items for M*K < 2^34
+  const int64_t nsb = K / 256;
+  const int64_t grid = (M + kTileRows - 1) / kTileRows * nsb;
+  hipLaunchKernelGGL(quantize_q8_1_tiled_kernel<ROWS>, dim3((unsigned)grid), dim3(64 * kTileWaves),
+                     0, s, reinterpret_cast<const float4*>(x), reinterpret_cast<uint32_t*>(base),
+                     reinterpret_cast<uint32_t*>(base + M * K),
+                     reinterpret_cast<float*>(base + q8_planes_offset(M, K)),
+                     reinterpret_cast<uint16_t*>(base + q8_pieces_offset(M, K)),
+                     (uint32_t)M, (uint32_t)K, (uint32_t)nsb);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_quantize_rows(const float* x, int64_t M, int64_t K, void* q8, hipStream_t s) {
+  return launch_tiled<true>(x, M, K, q8, s);
+}
+
 hipError_t launch_quantize_q8_1(const float* x, int64_t M, int64_t K, void* q8, hipStream_t s) {
   uint8_t* base = static_cast<uint8_t*>(q8);
-  if (K % 256 == 0) {
-    // ceil(M/8) * K/256 workgroups of 256 work-items: below 2^31 work-items for M*K < 2^34
-    const int64_t nsb = K / 256;
-    const int64_t grid = (M + kTileRows - 1) / kTileRows * nsb;
-    hipLaunchKernelGGL(quantize_q8_1_tiled_kernel, dim3((unsigned)grid), dim3(64 * kTileWaves),
-                       0, s, reinterpret_cast<const float4*>(x), reinterpret_cast<uint32_t*>(base),
-                       reinterpret_cast<uint32_t*>(base + M * K),
-                       reinterpret_cast<float*>(base + q8_planes_offset(M, K)),
-                       reinterpret_cast<uint16_t*>(base + q8_pieces_offset(M, K)),
-                       (uint32_t)M, (uint32_t)K, (uint32_t)nsb);
-    return hipGetLastError();
-  }
+  if (K % 256 == 0) return launch_tiled<false>(x, M, K, q8, s);
   const int64_t nblocks = M * (K / 32);
   const int64_t waves = (nblocks + 8 * kGroups - 1) / (8 * kGroups);
   const int64_t grid = (waves + 3) / 4;
