@@ -189,8 +189,9 @@ int mmq_q4K_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const flo
  * The mixture-of-experts layer for more tokens than a plan takes, and for any raggedness: the
  * (token, slot) pairs p = t*k + s are sorted by expert on the device, and one launch runs each
  * expert's rows, however many, against its matrix. Nothing about the counts has to be known on the
- * host. Per pair the products are, bit for bit, what mmq_q4K_q8_1_ex computes for its row and its
- * expert's matrix with MMQ_TILE_LARGE (or HALF, MEDIUM, SMALL) and one split.
+ * host. Per pair the products are mmq_q4K_q8_1's for its row and its expert's matrix, within the same
+ * bound; the order in which K is added up depends on M, E, k, N and K (and the device's compute units),
+ * not on the ids.
  *
  * Limits of all of them: 1 <= M*k <= 2^21, E <= 512, k <= min(E, 64).
  */

@@ -21,6 +21,10 @@
 //   read per 33 vector instructions.) Tokens are quantized once, not once per slot.
 // - Workgroups go to the XCDs in turn. Each XCD gets a contiguous range of the tiles in the order
 //   (weight-tile group, expert, rows), so the row tiles that share weights run on one L2.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
 #include "epilogue.h"
 #include "grouped_internal.h"
 #include "mmq_device.h"
@@ -35,281 +39,379 @@ __device__ __forceinline__ void set_priority(int p) {
   else __builtin_amdgcn_s_setprio(0);
 }
 
-constexpr int kNW = 8;  // wavefronts of a workgroup, one 32-row weight tile each
+// The shape of a workgroup: CW wavefronts side by side, one 32-row weight tile each, for every of KS
+// ranges of K, and TMAX 32-row parts of an expert's rows at most; WAVES wavefronts to a SIMD.
+template <int TMAX_, int CW_, int KS_, int WAVES_>
+struct Form {
+  static constexpr int TMAX = TMAX_, CW = CW_, KS = KS_, NW = CW_ * KS_, WAVES = WAVES_;
+  static constexpr int BM = 32 * TMAX;
+  static constexpr bool kLean = WAVES >= 4;  // 128 registers to a wavefront
+  // One stage: per range of K the int8 token tile [BM][272], the (da, nb) pairs [4][BM][2 blocks][2]
+  // and the token pieces [3][BM][8]; then the wavefronts' 32 row headers. Behind the two stages the
+  // expanded weight scales, which only their wavefront uses, one super-block at a time; then the
+  // tile's rows, each its pair and its row of the q8 buffer.
+  static constexpr int kTokA = BM * kRowStride, kTokDa = BM * 64, kTokP = BM * 48;
+  static constexpr int kTokens = kTokA + kTokDa + kTokP;
+  static constexpr int kStage = KS * kTokens + NW * kRepHdrBytes;
+  static constexpr int kExpanded = kWDsvBytes + kWPieceBytes;
+  static constexpr int kRowsAt = 2 * kStage + NW * kExpanded;
+  static constexpr int kLds = kRowsAt + BM * (int)sizeof(int2);
+  static constexpr int kADma = (BM * (kRowStride / 16) + 63) / 64;  // wavefront-wide instructions
+  static constexpr int kDaDma = (4 * BM + 63) / 64, kPDma = (3 * BM + 63) / 64;
+  static constexpr int kAOps = (kADma + CW - 1) / CW, kDaOps = (kDaDma + CW - 1) / CW;
+  static constexpr int kPOps = (kPDma + CW - 1) / CW;
+  // what a stage loads into LDS, as single instructions of a wavefront: its row headers and its share
+  // of the tokens
+  static constexpr int kOps = 1 + kAOps + kDaOps + kPOps;
+};
 
-// What a tile needs besides its rows.
-struct TileArgs {
+struct Args {
   const int8_t* qs;
   const float* da;
   const uint16_t* pieces;
-  const uint8_t* w;   // the expert's records
+  const int* groups;
+  const uint8_t* w;
   float* out;
-  int q_rows, per_row, N, K, tn;
+  int P, E, N, K, q_rows, per_row, gn, order_at;
+  int most;  // the most tiles of a weight-tile group that the pairs can form
 };
 
-// One tile of 32 TT rows. rows[i] is the pair of row i, -1 past the tile's last row.
-template <int TT, int EPI>
-__device__ __forceinline__ void tile(uint8_t* smem, const int* rows, const TileArgs& g,
-                                     const EpiParam<EPI>& epi) {
-  constexpr int NW = kNW;
-  constexpr int BM = 32 * TT;
-  constexpr int NS = 8 * TT;                      // (block, token tile) steps per super-block
-  constexpr int A_BYTES = BM * kRowStride;        // token tile
-  constexpr int DA_BYTES = BM * 64;               // (da, nb) pairs [4][BM][2 blocks][2]
-  constexpr int TP_BYTES = BM * 48;               // token pieces of da*sa [3][BM][8]
-  constexpr int W_BYTES = kWDsvBytes + kWPieceBytes + kRepHdrBytes;
-  constexpr int STAGE = A_BYTES + DA_BYTES + TP_BYTES + NW * W_BYTES;
-  static_assert(STAGE == TileShape{TT, NW}.stage_bytes(), "LDS stage layout");
-  constexpr int A_SLOTS = BM * (kRowStride / 16);  // 16-byte slots of the token tile
-  constexpr int A_DMA = (A_SLOTS + 63) / 64;       // wavefront-wide DMA instructions
-  constexpr int A_PER_WAVE = (A_DMA + NW - 1) / NW;
-  constexpr int DA_SLOTS = 4 * BM;
-  constexpr int DA_DMA = (DA_SLOTS + 63) / 64;
-  constexpr int DA_PER_WAVE = (DA_DMA + NW - 1) / NW;
-  constexpr int TP_SLOTS = 3 * BM;
-  constexpr int TP_DMA = (TP_SLOTS + 63) / 64;
-  constexpr int TP_PER_WAVE = (TP_DMA + NW - 1) / NW;
+// A tile: its expert, its first row in the order, its rows (0: none) and its weight-tile group.
+struct Pick {
+  int expert, first, rows, tn;
+};
 
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = lane >> 5;
-  const int l32 = lane & 31;
+// The tile of this workgroup: each wavefront looks at 64 experts at a time, one to a lane. The offsets
+// are only used inside [0, P], so that groups of nonsense select nonsense rows of this product and no
+// others. In LDS before the first stage is loaded.
+struct SearchLds {
+  int totals[kGroupMaxExperts / 64];
+  Pick pick;
+};
+template <class F>
+__device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
+  constexpr int NCH = kGroupMaxExperts / 64, CH = (NCH + F::NW - 1) / F::NW;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int lo[CH], n[CH], incl[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int e = (wave + c * F::NW) * 64 + lane;
+    lo[c] = n[c] = 0;
+    if (e < g.E) {
+      lo[c] = min(max(g.groups[e], 0), g.P);
+      n[c] = min(max(g.groups[e + 1], lo[c]), g.P) - lo[c];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    incl[c] = (n[c] + F::BM - 1) / F::BM;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(incl[c], d);
+      if (lane >= d) incl[c] += o;
+    }
+    if (lane == 63 && wave + c * F::NW < NCH) sh.totals[wave + c * F::NW] = incl[c];
+  }
+  if (threadIdx.x == 0) sh.pick.rows = 0;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < NCH; ++w) {
+    const int v = sh.totals[w];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (w < wave + c * F::NW) incl[c] += v;
+    all += v;
+  }
+  all = min(all, g.most);  // what the grid covers (offsets of nonsense may ask for more)
+  // tiles in the order (weight-tile group, expert, rows), one contiguous range per XCD
+  const unsigned total = (unsigned)all * (unsigned)g.gn;
+  const unsigned per_xcd = (total + 7u) >> 3;
+  const unsigned k = blockIdx.x >> 3;
+  const unsigned idx = (blockIdx.x & 7u) * per_xcd + k;
+  if (k < per_xcd && idx < total) {
+    const int tn = (int)(idx / (unsigned)all);
+    const int at = (int)(idx - (unsigned)tn * (unsigned)all);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int mine = (n[c] + F::BM - 1) / F::BM;
+      const int u = at - (incl[c] - mine);
+      if (u >= 0 && u < mine)
+        sh.pick = Pick{(wave + c * F::NW) * 64 + lane, lo[c] + u * F::BM,
+                       min(n[c] - u * F::BM, F::BM), tn};
+    }
+  }
+  __syncthreads();
+  const Pick p = sh.pick;
+  return Pick{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.first),
+              __builtin_amdgcn_readfirstlane(p.rows), __builtin_amdgcn_readfirstlane(p.tn)};
+}
 
-  const int N = g.N, K = g.K;
-  const int ntiles = (N + 31) >> 5;
-  const int wt_raw = g.tn * NW + wave;
-  const bool wt_ok = wt_raw < ntiles;
-  const int wt = wt_ok ? wt_raw : ntiles - 1;  // idle wavefronts still stage and sync
-  const int nsb = K >> 8;
-  const uint32_t M = (uint32_t)g.q_rows;
-  const uint32_t q_bytes = M * (uint32_t)K;
-  const uint32_t da_bytes = q_bytes >> 2;
-  const uint32_t tp_bytes = M * (uint32_t)nsb * 48u;
-  const v4i rq = make_rsrc_sgpr(g.qs, q_bytes);
-  const v4i rda = make_rsrc_sgpr(g.da, da_bytes);
-  const v4i rtp = make_rsrc_sgpr(g.pieces, tp_bytes);
-  const uint8_t* wtile = g.w + (size_t)wt * nsb * kRepTileBytes;
-  const v4i rwd = make_rsrc_sgpr(wtile, (uint32_t)nsb * kRepTileBytes);
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(wtile, (uint32_t)nsb * kRepTileBytes);
+// The rows of a tile, each its pair and its row of the q8 buffer; -1 and the buffer's end past the last.
+template <class F>
+__device__ __forceinline__ int2 load_row(const Args& g, const Pick& t) {
+  const int i = threadIdx.x;
+  int p = -1;
+  if (i < t.rows) p = g.groups[g.order_at + t.first + i];
+  if (p < 0 || p >= g.P) return make_int2(-1, g.q_rows);
+  return make_int2(p, (int)((unsigned)p / (unsigned)g.per_row));
+}
 
-  // The row of the q8 buffer of the tile's row r; none (the buffers' end, which reads zero) past it.
-  auto src_of = [&](int r) -> uint32_t {
-    const int p = rows[r];
-    return p < 0 ? M : (uint32_t)p / (uint32_t)g.per_row;
-  };
-  // Token-tile DMA slots of this lane: slot q = 64*k + lane holds chunk q % 17 of row q / 17;
-  // chunk 16 is the row's padding and reads past the end (zero), as do rows past the last.
-  uint32_t a_off[A_PER_WAVE];
-  bool a_act[A_PER_WAVE];
-#pragma unroll
-  for (int j = 0; j < A_PER_WAVE; ++j) {
-    const int k = wave + j * NW;
-    const int q = k * 64 + lane;
-    const int row = q / 17, c = q - row * 17;
-    a_act[j] = k < A_DMA && q < A_SLOTS;
-    const uint32_t src = a_act[j] ? src_of(row) : M;
-    a_off[j] = c < 16 && src < M ? src * (uint32_t)K + c * 16 : q_bytes;
+// What a wavefront loads for a tile.
+template <class F>
+struct Loads {
+  v4i rq, rda, rtp, rwd;
+  __amdgpu_buffer_rsrc_t rw;
+  uint32_t a_off[F::kAOps], da_off[F::kDaOps], tp_off[F::kPOps];
+  uint32_t tp_step;
+  int parts, cw, wave, lane;
+  bool works;  // whether the wavefront has a weight tile
+  uint32_t lds0, tok_at, hdr_at;
+
+  __device__ __forceinline__ void init(const uint8_t* smem, const Args& g) {
+    const uint32_t M = (uint32_t)g.q_rows, K = (uint32_t)g.K;
+    rq = make_rsrc_sgpr(g.qs, M * K);
+    rda = make_rsrc_sgpr(g.da, M * K >> 2);
+    rtp = make_rsrc_sgpr(g.pieces, M * (K >> 8) * 48u);
+    tp_step = M * 48u;
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    cw = F::KS == 1 ? wave : wave % F::CW;
+    lds0 = lds_addr(smem);
+    tok_at = (uint32_t)((F::KS == 1 ? 0 : wave / F::CW) * F::kTokens);
+    hdr_at = (uint32_t)(F::KS * F::kTokens + wave * kRepHdrBytes);
   }
-  // (da, nb): slot q holds pair of blocks q / BM of row q % BM; 64 bytes per row and super-block.
-  uint32_t da_off[DA_PER_WAVE];
-  bool da_act[DA_PER_WAVE];
-#pragma unroll
-  for (int j = 0; j < DA_PER_WAVE; ++j) {
-    const int k = wave + j * NW;
-    const int q = k * 64 + lane;
-    const int bp = q / BM, r = q - bp * BM;
-    da_act[j] = k < DA_DMA && q < DA_SLOTS;
-    const uint32_t src = da_act[j] ? src_of(r) : M;
-    da_off[j] = src < M ? src * ((uint32_t)K >> 2) + bp * 16 : da_bytes;
+  // The tile's weights.
+  __device__ __forceinline__ void aim(const Args& g, const Pick& t) {
+    const int ntiles = (g.N + 31) >> 5;
+    works = t.tn * F::CW + cw < ntiles;  // one without loads tokens for the others
+    const int wt = works ? t.tn * F::CW + cw : ntiles - 1;
+    const size_t tile_bytes = (size_t)(g.K >> 8) * kRepTileBytes;
+    const uint8_t* wtile = g.w + ((size_t)t.expert * ntiles + wt) * tile_bytes;
+    rwd = make_rsrc_sgpr(wtile, (uint32_t)tile_bytes);
+    rw = make_rsrc(wtile, (uint32_t)tile_bytes);
+    parts = (t.rows + 31) >> 5;
   }
-  // Token pieces: slot q holds piece q / BM of row q % BM; [super-block][piece][M][8] in memory. A
-  // row past the last starts at the end of the plane, and stays past it with every super-block.
-  uint32_t tp_off[TP_PER_WAVE];
-  bool tp_act[TP_PER_WAVE];
+  // Its tokens: a row past the last, and the padding, read past the buffers' ends (zero), and stay there
+  // with every super-block.
+  __device__ __forceinline__ void aim(const Args& g, const int2* rows) {
+    const uint32_t M = (uint32_t)g.q_rows, K = (uint32_t)g.K;
 #pragma unroll
-  for (int j = 0; j < TP_PER_WAVE; ++j) {
-    const int k = wave + j * NW;
-    const int q = k * 64 + lane;
-    const int pc = q / BM, r = q - pc * BM;
-    tp_act[j] = k < TP_DMA && q < TP_SLOTS;
-    const uint32_t src = tp_act[j] ? src_of(r) : M;
-    tp_off[j] = src < M ? ((uint32_t)pc * M + src) * 16u : tp_bytes;
+    for (int j = 0; j < F::kAOps; ++j) {  // slot q holds chunk q % 17 of row q / 17
+      const int q = (cw + j * F::CW) * 64 + lane;
+      const int row = q / 17, c = q - row * 17;
+      const uint32_t src = row < F::BM ? (uint32_t)rows[row].y : M;
+      a_off[j] = c < 16 && src < M ? src * K + c * 16 : M * K;
+    }
+#pragma unroll
+    for (int j = 0; j < F::kDaOps; ++j) {  // pair of blocks q / BM of row q % BM
+      const int q = (cw + j * F::CW) * 64 + lane;
+      const uint32_t src = q < 4 * F::BM ? (uint32_t)rows[q % F::BM].y : M;
+      da_off[j] = src < M ? src * (K >> 2) + (q / F::BM) * 16 : M * K >> 2;
+    }
+#pragma unroll
+    for (int j = 0; j < F::kPOps; ++j) {  // piece q / BM of row q % BM
+      const int q = (cw + j * F::CW) * 64 + lane;
+      const uint32_t src = q < 3 * F::BM ? (uint32_t)rows[q % F::BM].y : M;
+      tp_off[j] = src < M ? ((uint32_t)(q / F::BM) * M + src) * 16u : M * (K >> 8) * 48u;
+    }
   }
-  // What a stage loads into LDS, as NOPS - 1 DMA instructions of this wavefront, and, as the last
-  // op, its last 16 bytes of nibbles into registers; spread over the previous super-block's steps as
-  // in mmq_gemm.hip.
-  constexpr int NOPS = A_PER_WAVE + DA_PER_WAVE + TP_PER_WAVE + 2;
-  auto op_step = [](int v) { return ((v / 3) * 2 * TT < NS - 1) ? (v / 3) * 2 * TT : NS - 1; };
-  auto load_nib = [&](int s, int gi) -> v4i {
-    return buf_load16(rw, (uint32_t)s * kRepTileBytes + gi * 1024 + lane * 16);
-  };
-  const uint32_t lds0 = lds_addr(smem);
-  auto issue_op = [&](int v, int s, int p, v4i& nib3) {
-    const uint32_t st = lds0 + (uint32_t)(p * STAGE);
-    if (v < A_PER_WAVE) {
-      const int k = wave + v * NW;
-      if (k < A_DMA && a_act[v]) dma16(rq, st + k * 1024, a_off[v] + (uint32_t)s * 256);
-      return;
-    }
-    v -= A_PER_WAVE;
-    if (v < DA_PER_WAVE) {
-      const int k = wave + v * NW;
-      if (k < DA_DMA && da_act[v])
-        dma16(rda, st + A_BYTES + k * 1024, da_off[v] + (uint32_t)s * 64);
-      return;
-    }
-    v -= DA_PER_WAVE;
-    if (v < TP_PER_WAVE) {
-      const int k = wave + v * NW;
-      if (k < TP_DMA && tp_act[v])
-        dma16(rtp, st + A_BYTES + DA_BYTES + k * 1024, tp_off[v] + (uint32_t)s * 3u * M * 16u);
-      return;
-    }
-    v -= TP_PER_WAVE;
+  // Instruction v of super-block s into stage p; those of parts that the tile does not have are left out.
+  __device__ __forceinline__ void issue(int v, int s, int p) const {
+    const uint32_t st = lds0 + (uint32_t)p * F::kStage + tok_at;
     if (v < 1) {
-      const uint32_t sw = st + A_BYTES + DA_BYTES + TP_BYTES + wave * W_BYTES;
       if (lane < 32)
-        dma16(rwd, sw + kWDsvBytes + kWPieceBytes,
+        dma16(rwd, lds0 + (uint32_t)p * F::kStage + hdr_at,
               (uint32_t)s * kRepTileBytes + kRepNibBytes + lane * 16);
       return;
     }
-    nib3 = load_nib(s, 3);
-  };
+    v -= 1;
+    if (v < F::kAOps) {
+      const int k = cw + v * F::CW;
+      if (k * 64 < parts * (32 * 17)) dma(rq, st, k, F::BM * 17, a_off[v] + (uint32_t)s * 256);
+      return;
+    }
+    v -= F::kAOps;
+    if (v < F::kDaOps) {
+      const int k = cw + v * F::CW;
+      if (k < F::kDaDma) dma(rda, st + F::kTokA, k, 4 * F::BM, da_off[v] + (uint32_t)s * 64);
+      return;
+    }
+    v -= F::kDaOps;
+    const int k = cw + v * F::CW;
+    if (k < F::kPDma)
+      dma(rtp, st + F::kTokA + F::kTokDa, k, 3 * F::BM, tp_off[v] + (uint32_t)s * tp_step);
+  }
+  // slots 64 k .. 64 k + 63, of which `slots` exist
+  __device__ __forceinline__ void dma(v4i r, uint32_t lds, int k, int slots, uint32_t off) const {
+    if (k * 64 + lane < slots) dma16(r, lds + k * 1024, off);
+  }
+  __device__ __forceinline__ v4i nibbles(int s, int gi) const {
+    return buf_load16(rw, (uint32_t)s * kRepTileBytes + gi * 1024 + lane * 16);
+  }
+};
 
+// The sums of a tile of TT parts over super-blocks s0 .. s1 - 1, the first of which is in stage 0 and, its
+// nibbles, in raw; `steps` barriers.
+template <class F, int TT>
+__device__ __forceinline__ void sums(uint8_t* smem, const Loads<F>& ld, int s0, int s1, int steps,
+                                     v4i (&raw)[4], v16f (&acc)[TT]) {
+  constexpr int NS = 8 * TT;  // (block, token tile) steps per super-block
+  constexpr bool LEAN = F::kLean;
+  const int lane = ld.lane, h = lane >> 5, l32 = lane & 31;
+  // The next stage's instructions are spread over a super-block's steps, three at a time, as in
+  // mmq_gemm.hip.
+  auto op_step = [](int v) { return ((v / 3) * 2 * TT < NS - 1) ? (v / 3) * 2 * TT : NS - 1; };
   v16i bias;
 #pragma unroll
   for (int r = 0; r < 16; ++r) bias[r] = kBiasBits;
   asm volatile("" : "+v"(bias));  // stays in vector registers, as in mmq_gemm.hip
-  v16f acc[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[t][r] = 0.0f;
 
-  // The nibbles of the next stage: in place as they are used up, or (one token tile: a super-block is
-  // too short for that) all at the first step, through a second set. As in mmq_gemm.hip.
+  // The nibbles of the next stage: in place as they are used up (the last through nib3), or, where a
+  // super-block is too short for that (one token tile), all at the first step through a second set.
   constexpr bool ENIB = TT == 1;
-  v4i raw[4], nib3, rawB[ENIB ? 4 : 1];
-#pragma unroll
-  for (int v = 0; v < NOPS - (ENIB ? 1 : 0); ++v) issue_op(v, 0, 0, nib3);
-#pragma unroll
-  for (int gi = 0; gi < (ENIB ? 4 : 3); ++gi) raw[gi] = load_nib(0, gi);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-
-  for (int s = 0; s < nsb; ++s) {
-    const int p = s & 1;
+  v4i nib3 = raw[3], rawB[ENIB ? 4 : 1];
+  for (int i = 0; i < steps; ++i) {
+    const int s = s0 + i, p = i & 1;
     if constexpr (!ENIB) raw[3] = nib3;
-    const bool more = s + 1 < nsb;
-
-    const uint8_t* st = smem + p * STAGE;
-    const uint8_t* sArow = st + l32 * kRowStride + h * 16;
-    const uint8_t* sDa = st + A_BYTES;
-    const uint8_t* sTp = st + A_BYTES + DA_BYTES;
-    const uint8_t* sW = st + A_BYTES + DA_BYTES + TP_BYTES + wave * W_BYTES;
-    const float* sWw = reinterpret_cast<const float*>(sW);
-    auto expand_scales = [&]() {
-      uint8_t* sWm = smem + p * STAGE + A_BYTES + DA_BYTES + TP_BYTES + wave * W_BYTES;
-      const v4i hdr =
-          *reinterpret_cast<const v4i*>(sWm + kWDsvBytes + kWPieceBytes + l32 * 16);
-      q4k_stage_scales(hdr, l32, h != 0, sWm);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    };
-    auto wop_of = [&](int b) -> v4i {
-      const v4i rr = raw[b >> 1];
-      return (b & 1) ? ((rr >> 4) & 0x0F0F0F0F) : (rr & 0x0F0F0F0F);
-    };
-    auto top_of = [&](int n) -> v4i {
-      const int b = n / TT, t = n % TT;
-      return *reinterpret_cast<const v4i*>(sArow + t * 32 * kRowStride + b * 32);
-    };
-    auto da_of = [&](int n) -> float2 {
-      const int b = n / TT, t = n % TT;
-      return *reinterpret_cast<const float2*>(sDa + ((b >> 1) * BM + t * 32 + l32) * 16 +
-                                              (b & 1) * 8);
-    };
-    auto dsv_of = [&](int b, float (&d)[16]) {
+    const bool more = s + 1 < s1;
+    if ((F::KS == 1 || s < s1) && ld.works) {
+      const uint8_t* st = smem + p * F::kStage + ld.tok_at;
+      const uint8_t* sArow = st + l32 * kRowStride + h * 16;
+      const uint8_t* sDa = st + F::kTokA;
+      const uint8_t* sTp = st + F::kTokA + F::kTokDa;
+      uint8_t* sW = smem + 2 * F::kStage + ld.wave * F::kExpanded;
+      const float* sWw = reinterpret_cast<const float*>(sW);
+      // (the wavefront's reads of the last super-block's scales came before the barrier)
+      auto expand_scales = [&]() {
+        const v4i hdr =
+            *reinterpret_cast<const v4i*>(smem + p * F::kStage + ld.hdr_at + l32 * 16);
+        q4k_stage_scales(hdr, l32, h != 0, sW);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      };
+      auto wop_of = [&](int b) -> v4i {
+        const v4i rr = raw[b >> 1];
+        return (b & 1) ? ((rr >> 4) & 0x0F0F0F0F) : (rr & 0x0F0F0F0F);
+      };
+      auto top_of = [&](int n) -> v4i {
+        const int b = n / TT, t = n % TT;
+        return *reinterpret_cast<const v4i*>(sArow + t * 32 * kRowStride + b * 32);
+      };
+      auto da_of = [&](int n) -> float2 {
+        const int b = n / TT, t = n % TT;
+        return *reinterpret_cast<const float2*>(sDa + ((b >> 1) * F::BM + t * 32 + l32) * 16 +
+                                                (b & 1) * 8);
+      };
+      auto dsv_of = [&](int b, float (&d)[16]) {
 #pragma unroll
-      for (int gi = 0; gi < 4; ++gi) {
-        const float4 a = *reinterpret_cast<const float4*>(sWw + b * 32 + 8 * gi + 4 * h);
-        d[4 * gi + 0] = a.x; d[4 * gi + 1] = a.y; d[4 * gi + 2] = a.z; d[4 * gi + 3] = a.w;
+        for (int gi = 0; gi < 4; ++gi) {
+          const float4 a = *reinterpret_cast<const float4*>(sWw + b * 32 + 8 * gi + 4 * h);
+          d[4 * gi + 0] = a.x; d[4 * gi + 1] = a.y; d[4 * gi + 2] = a.z; d[4 * gi + 3] = a.w;
+        }
+      };
+
+      // Entering step n = b*TT + t: D(n) has been issued, the token operand of step n+1 and da of
+      // step n are in registers; dsv[b & 1] holds block b's weight scales. LEAN, four wavefronts to a
+      // SIMD: the others cover a step's latency instead.
+      v16i Dn;
+      v4i tnext;
+      float2 da;
+      float dsv[LEAN ? 1 : 2][16];
+      if constexpr (!LEAN) {
+        Dn = __builtin_amdgcn_mfma_i32_32x32x32_i8(wop_of(0), top_of(0), bias, 0, 0, 0);
+        asm volatile("" : "+v"(Dn));  // issued here, not sunk below the expansion
+        tnext = top_of(1 % NS);
+        da = da_of(0);
       }
-    };
-
-    // Entering step n = b*TT + t: D(n) has been issued, the token operand of step n+1 and da of
-    // step n are in registers; dsv[b & 1] holds block b's weight scales.
-    v16i Dn = __builtin_amdgcn_mfma_i32_32x32x32_i8(wop_of(0), top_of(0), bias, 0, 0, 0);
-    asm volatile("" : "+v"(Dn));  // issued here, not sunk below the expansion
-    v4i tnext = top_of(1 % NS);
-    float2 da = da_of(0);
-    expand_scales();
-    float dsv[2][16];
-    dsv_of(0, dsv[0]);
+      expand_scales();
+      dsv_of(0, dsv[0]);
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      const int b = n / TT, t = n % TT;
-      if (n % 2 == 0) set_priority(3 - (n % 8) / 2);  // the pair of a SIMD keeps step
-      if (more) {
-        if constexpr (ENIB) {
-          if (n == 0) {
+      for (int n = 0; n < NS; ++n) {
+        const int b = n / TT, t = n % TT;
+        if (n % 2 == 0) set_priority(3 - (n % 8) / 2);  // the pair of a SIMD keeps step
+        if (more) {
+          if constexpr (ENIB) {
+            if (n == 0) {
 #pragma unroll
-            for (int gi = 0; gi < 4; ++gi) rawB[gi] = load_nib(s + 1, gi);
+              for (int gi = 0; gi < 4; ++gi) rawB[gi] = ld.nibbles(s + 1, gi);
+            }
           }
 #pragma unroll
-          for (int v = 0; v < NOPS - 1; ++v)
-            if (op_step(v) == n) issue_op(v, s + 1, p ^ 1, nib3);
+          for (int v = 0; v < F::kOps; ++v)
+            if (op_step(v) == n) ld.issue(v, s + 1, p ^ 1);
+          if constexpr (!ENIB) {
+            if (op_step(F::kOps) == n) nib3 = ld.nibbles(s + 1, 3);
+#pragma unroll
+            for (int gi = 0; gi < 3; ++gi)
+              if (n == (2 * gi + 2) * TT) raw[gi] = ld.nibbles(s + 1, gi);
+          }
+        }
+        v16i D;
+        float2 dac;  // (da, nb)
+        if constexpr (LEAN) {
+          v4i top = top_of(n);
+          asm volatile("" : "+v"(top));  // the steps stay in order
+          D = __builtin_amdgcn_mfma_i32_32x32x32_i8(wop_of(b), top, bias, 0, 0, 0);
+          dac = da_of(n);
+          if (t == 0 && b > 0) dsv_of(b, dsv[0]);
         } else {
+          D = Dn;
+          dac = da;
+          if (n + 1 < NS) {
+            Dn = __builtin_amdgcn_mfma_i32_32x32x32_i8(wop_of((n + 1) / TT), tnext, bias, 0, 0, 0);
+            da = da_of(n + 1);
+          }
+          if (n + 2 < NS) tnext = top_of(n + 2);
+          if (t == 0 && b + 1 < 8) dsv_of(b + 1, dsv[(b + 1) & 1]);
+        }
 #pragma unroll
-          for (int v = 0; v < NOPS; ++v)
-            if (op_step(v) == n) issue_op(v, s + 1, p ^ 1, nib3);
-#pragma unroll
-          for (int gi = 0; gi < 3; ++gi)
-            if (n == (2 * gi + 2) * TT) raw[gi] = load_nib(s + 1, gi);
+        for (int r = 0; r < 16; ++r) {
+          const float y = __builtin_fmaf(__int_as_float(D[r]), dac.x, dac.y);
+          acc[t][r] = __builtin_fmaf(y, dsv[LEAN ? 0 : b & 1][r], acc[t][r]);
+        }
+        if (b == 1 || b == 3 || b == 5) {  // a third of term2, the piece pairs of mmq_gemm.hip
+          const int u = b >> 1;
+          const int ia = u == 0 ? 0 : (u == 1 ? 1 - h : 1 + h);
+          const int jb = u == 0 ? h : (u == 1 ? 2 * h : 1 - h);
+          const v8bf wa = *reinterpret_cast<const v8bf*>(sW + kWDsvBytes + (ia * 32 + l32) * 16);
+          const v8bf tb =
+              *reinterpret_cast<const v8bf*>(sTp + (jb * F::BM + t * 32 + l32) * 16);
+          acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, tb, acc[t], 0, 0, 0);
         }
       }
-      const v16i D = Dn;
-      const float2 dac = da;  // (da, nb)
-      if (n + 1 < NS) {
-        Dn = __builtin_amdgcn_mfma_i32_32x32x32_i8(wop_of((n + 1) / TT), tnext, bias, 0, 0, 0);
-        da = da_of(n + 1);
-      }
-      if (n + 2 < NS) tnext = top_of(n + 2);
-      if (t == 0 && b + 1 < 8) dsv_of(b + 1, dsv[(b + 1) & 1]);
+    } else if (more) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float y = __builtin_fmaf(__int_as_float(D[r]), dac.x, dac.y);
-        acc[t][r] = __builtin_fmaf(y, dsv[b & 1][r], acc[t][r]);
-      }
-      if (b == 1 || b == 3 || b == 5) {  // a third of term2, the piece pairs of mmq_gemm.hip
-        const int u = b >> 1;
-        const int ia = u == 0 ? 0 : (u == 1 ? 1 - h : 1 + h);
-        const int jb = u == 0 ? h : (u == 1 ? 2 * h : 1 - h);
-        const v8bf wa = *reinterpret_cast<const v8bf*>(sW + kWDsvBytes + (ia * 32 + l32) * 16);
-        const v8bf tb = *reinterpret_cast<const v8bf*>(sTp + (jb * BM + t * 32 + l32) * 16);
-        acc[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa, tb, acc[t], 0, 0, 0);
-      }
+      for (int v = 0; v < F::kOps; ++v) ld.issue(v, s + 1, p ^ 1);
     }
 
     __builtin_amdgcn_s_setprio(0);
-    __builtin_amdgcn_s_waitcnt(0);  // this wavefront's stage s+1 loads have landed
-    __syncthreads();                // ... and everyone's; stage s is no longer read
+    __builtin_amdgcn_s_waitcnt(0);  // this wavefront's loads of the next stage have landed
+    __syncthreads();                // ... and everyone's; this stage is no longer read
     if constexpr (ENIB) {
 #pragma unroll
       for (int gi = 0; gi < 4; ++gi) raw[gi] = rawB[gi];
     }
   }
+}
 
-  // Out through the wavefront's own LDS regions, as in mmq_gemm.hip; a row's address is its pair's.
-  float* out = g.out;
+// Out through a transpose in the wavefront's own 32 x 20 floats of LDS, 16 columns at a time: four lanes
+// to a row's 64 bytes. A row's address is its pair's.
+template <class F, int TT, int EPI>
+__device__ __forceinline__ void store(float* reg, const int2* rows, const Args& g, int wt, int lane,
+                                      const v16f (&acc)[TT], const EpiParam<EPI>& epi) {
+  const int h = lane >> 5, l32 = lane & 31;
+  const bool wt_ok = wt < (g.N + 31) >> 5;
   if constexpr (EPI == kEpiGated) {
     constexpr int TS = 20;
-    const int F = epi.F;
+    const int cols = epi.F;
     const int rr = lane >> 2, c4 = lane & 3;  // read-back: rows rr + 16 k, columns 4*c4..+3
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      float* reg = reinterpret_cast<float*>(smem) + ((t & 1) * NW + wave) * (32 * TS);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         float v[4];
@@ -325,198 +427,220 @@ __device__ __forceinline__ void tile(uint8_t* smem, const int* rows, const TileA
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int row = rr + 16 * k;
-          const int pair = rows[t * 32 + row];
+          const int pair = rows[t * 32 + row].x;
           const int j = wt * 16 + 4 * c4;
           if (pair < 0) continue;
           const float4 v = *reinterpret_cast<const float4*>(reg + row * TS + 4 * c4);
-          float* o = out + (size_t)pair * F + j;
-          if ((F & 3) == 0 && j + 3 < F) {
+          float* o = g.out + (size_t)pair * cols + j;
+          if ((cols & 3) == 0 && j + 3 < cols) {
             *reinterpret_cast<float4*>(o) = v;
           } else {
-            if (j + 0 < F) o[0] = v.x;
-            if (j + 1 < F) o[1] = v.y;
-            if (j + 2 < F) o[2] = v.z;
-            if (j + 3 < F) o[3] = v.w;
+            if (j + 0 < cols) o[0] = v.x;
+            if (j + 1 < cols) o[1] = v.y;
+            if (j + 2 < cols) o[2] = v.z;
+            if (j + 3 < cols) o[3] = v.w;
           }
         }
       }
-    }
-  } else {
-    constexpr int TS = 36;
-    const int rr = lane >> 3, c4 = lane & 7;  // read-back: rows rr + 8 k, columns 4*c4..+3
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      float* reg = reinterpret_cast<float*>(smem) + ((t & 1) * NW + wave) * (32 * TS);
-#pragma unroll
-      for (int gi = 0; gi < 4; ++gi)
-        *reinterpret_cast<float4*>(reg + l32 * TS + 8 * gi + 4 * h) = make_float4(
-            acc[t][4 * gi], acc[t][4 * gi + 1], acc[t][4 * gi + 2], acc[t][4 * gi + 3]);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
-      if (wt_ok) {
+    }
+  } else {
+    constexpr int TS = 20;
+    const int rr = lane >> 2, c4 = lane & 3;  // read-back: rows rr + 16 k, columns 4*c4..+3
+    const int N = g.N;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = rr + 8 * k;
-          const int pair = rows[t * 32 + row];
-          const int j = wt * 32 + 4 * c4;
-          if (pair < 0) continue;
-          float4 v = *reinterpret_cast<const float4*>(reg + row * TS + 4 * c4);
-          if (epi.act != kActNone) {
-            v.x = activate(v.x, epi.act); v.y = activate(v.y, epi.act);
-            v.z = activate(v.z, epi.act); v.w = activate(v.w, epi.act);
-          }
-          float* o = out + (size_t)pair * N + j;
-          if ((N & 3) == 0 && j + 3 < N) {
-            *reinterpret_cast<float4*>(o) = v;
-          } else {
-            if (j + 0 < N) o[0] = v.x;
-            if (j + 1 < N) o[1] = v.y;
-            if (j + 2 < N) o[2] = v.z;
-            if (j + 3 < N) o[3] = v.w;
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // 16 of the 32 columns
+#pragma unroll
+        for (int gi = 0; gi < 2; ++gi) {
+          const int r = 8 * half + 4 * gi;
+          *reinterpret_cast<float4*>(reg + l32 * TS + 8 * gi + 4 * h) =
+              make_float4(acc[t][r], acc[t][r + 1], acc[t][r + 2], acc[t][r + 3]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (wt_ok) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int row = rr + 16 * k;
+            const int pair = rows[t * 32 + row].x;
+            const int j = wt * 32 + 16 * half + 4 * c4;
+            if (pair < 0) continue;
+            float4 v = *reinterpret_cast<const float4*>(reg + row * TS + 4 * c4);
+            if (epi.act != kActNone) {
+              v.x = activate(v.x, epi.act); v.y = activate(v.y, epi.act);
+              v.z = activate(v.z, epi.act); v.w = activate(v.w, epi.act);
+            }
+            float* o = g.out + (size_t)pair * N + j;
+            if ((N & 3) == 0 && j + 3 < N) {
+              *reinterpret_cast<float4*>(o) = v;
+            } else {
+              if (j + 0 < N) o[0] = v.x;
+              if (j + 1 < N) o[1] = v.y;
+              if (j + 2 < N) o[2] = v.z;
+              if (j + 3 < N) o[3] = v.w;
+            }
           }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
     }
   }
 }
 
-// Which tile a workgroup has: 32-row parts of expert e, from its row `first` of the order on.
-struct Pick {
-  int expert, first, rows, tn;
-};
-
-// LDS of the search, over the stages (which are not in use yet).
-struct SearchLds {
-  int wave_tiles[kNW];
-  Pick pick;
-};
-
-// Work-item e looks at expert e. The offsets are only used inside [0, P], so that groups of nonsense
-// select nonsense rows of this product and no others.
-template <int TMAX>
-__device__ __forceinline__ Pick find_tile(SearchLds& sh, const int* __restrict__ groups, int P,
-                                          int E, int gn, int most) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int lo = 0, n = 0;
-  if (tid < E) {
-    lo = min(max(groups[tid], 0), P);
-    n = min(max(groups[tid + 1], lo), P) - lo;
-  }
-  const int mine = (n + 32 * TMAX - 1) / (32 * TMAX);
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 63) sh.wave_tiles[wave] = incl;
-  if (tid == 0) sh.pick.rows = 0;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kNW; ++w) {
-    const int v = sh.wave_tiles[w];
-    if (w < wave) before += v;
-    all += v;
-  }
-  all = min(all, most);  // what the grid covers (offsets of nonsense may ask for more)
-  // tiles in the order (weight-tile group, rows), one contiguous range per XCD
-  const unsigned total = (unsigned)all * (unsigned)gn;
-  const unsigned per_xcd = (total + 7u) >> 3;
-  const unsigned k = blockIdx.x >> 3;
-  const unsigned idx = (blockIdx.x & 7u) * per_xcd + k;
-  if (k < per_xcd && idx < total) {
-    const int tn = (int)(idx / (unsigned)all);
-    const int u = (int)(idx - (unsigned)tn * (unsigned)all) - (before + incl - mine);
-    if (u >= 0 && u < mine)
-      sh.pick = Pick{tid, lo + u * 32 * TMAX, min(n - u * 32 * TMAX, 32 * TMAX), tn};
-  }
-  __syncthreads();
-  const Pick p = sh.pick;
-  return Pick{__builtin_amdgcn_readfirstlane(p.expert), __builtin_amdgcn_readfirstlane(p.first),
-              __builtin_amdgcn_readfirstlane(p.rows), __builtin_amdgcn_readfirstlane(p.tn)};
-}
-
-template <int TMAX, int EPI>
-__global__ __launch_bounds__(kNW * 64, 1) void grouped_kernel(
-    const int8_t* __restrict__ qs, const float* __restrict__ da, const uint16_t* __restrict__ pieces,
-    const int* __restrict__ groups, const uint8_t* __restrict__ w, float* __restrict__ out, int P,
-    int E, int N, int K, int q_rows, int per_row, int gn, int most, int order_at, EpiParam<EPI> epi) {
-  constexpr TileShape ts{TMAX, kNW};
+template <class F, int EPI>
+__global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, EpiParam<EPI> epi) {
   extern __shared__ __align__(16) uint8_t smem[];
-  int* rows = reinterpret_cast<int*>(smem + ts.lds_bytes());
-  const Pick pick = find_tile<TMAX>(*reinterpret_cast<SearchLds*>(smem), groups, P, E, gn, most);
-  if (pick.rows <= 0) return;
+  static_assert(F::BM <= 64 * F::NW, "a work-item per row");
   const int tid = threadIdx.x;
-  if (tid < 32 * TMAX) {
-    const int p = tid < pick.rows ? groups[order_at + pick.first + tid] : -1;
-    rows[tid] = p < P ? p : -1;
+  int2* rows = reinterpret_cast<int2*>(smem + F::kRowsAt);
+  const Pick t = find_tile<F>(*reinterpret_cast<SearchLds*>(smem), g);
+  if (t.rows <= 0) return;
+  int2 row;
+  if (tid < F::BM) row = load_row<F>(g, t);
+  Loads<F> ld;
+  ld.init(smem, g);
+  ld.aim(g, t);
+  const int nsb = g.K >> 8;
+  const int ks = F::KS == 1 ? 0 : ld.wave / F::CW;
+  const int s0 = F::KS == 1 ? 0 : ks * nsb / F::KS, s1 = F::KS == 1 ? nsb : (ks + 1) * nsb / F::KS;
+  const int steps = F::KS == 1 ? nsb : (nsb + F::KS - 1) / F::KS;  // the longest range's
+  const bool any = F::KS == 1 || s0 < s1;
+  v4i raw[4];
+  if (any) {  // the weights while the rows are on their way
+#pragma unroll
+    for (int gi = 0; gi < 4; ++gi) raw[gi] = ld.nibbles(s0, gi);
   }
+  if (tid < F::BM) rows[tid] = row;
   __syncthreads();
-  const size_t matrix = (size_t)((N + 31) >> 5) * (size_t)(K >> 8) * kRepTileBytes;
-  const TileArgs g{qs, da, pieces, w + (size_t)pick.expert * matrix, out, q_rows, per_row, N, K,
-                   pick.tn};
-  const int parts = (pick.rows + 31) >> 5;
-  if constexpr (TMAX >= 4) {
-    if (parts == 4) return tile<4, EPI>(smem, rows, g, epi);
-    if (parts == 3) return tile<3, EPI>(smem, rows, g, epi);
+  ld.aim(g, rows);
+  if (any) {
+#pragma unroll
+    for (int v = 0; v < F::kOps; ++v) ld.issue(v, s0, 0);
   }
-  if constexpr (TMAX >= 2) {
-    if (parts == 2) return tile<2, EPI>(smem, rows, g, epi);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  auto run = [&](auto parts) {
+    constexpr int TT = decltype(parts)::value;
+    v16f acc[TT];
+    sums<F, TT>(smem, ld, s0, s1, steps, raw, acc);
+    if constexpr (F::KS > 1) {
+      // the other ranges' sums, [range][wavefront][part][register][lane], added in the order of the
+      // ranges
+      static_assert((F::KS - 1) * F::CW * TT * 4096 <= 2 * F::kStage, "LDS of the sums");
+      float* red = reinterpret_cast<float*>(smem) + ld.lane;
+      if (ks > 0) {
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            red[((((ks - 1) * F::CW + ld.cw) * TT + u) * 16 + r) * 64] = acc[u][r];
+      }
+      __syncthreads();
+      if (ks > 0) return;
+#pragma unroll
+      for (int o = 0; o < F::KS - 1; ++o)
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            acc[u][r] += red[(((o * F::CW + ld.cw) * TT + u) * 16 + r) * 64];
+    }
+    // through the wavefront's region of weight scales
+    store<F, TT, EPI>(reinterpret_cast<float*>(smem + 2 * F::kStage + ld.wave * F::kExpanded), rows, g,
+                      t.tn * F::CW + ld.cw, ld.lane, acc, epi);
+  };
+  using std::integral_constant;
+  if constexpr (F::TMAX == 4) {
+    if (ld.parts == 4) return run(integral_constant<int, 4>{});
+    if (ld.parts == 3) return run(integral_constant<int, 3>{});
+    if (ld.parts == 2) return run(integral_constant<int, 2>{});
   }
-  tile<1, EPI>(smem, rows, g, epi);
+  static_assert(F::TMAX == 1 || F::TMAX == 4, "the numbers of parts");
+  run(integral_constant<int, 1>{});
 }
 
-constexpr int64_t lds_bytes(int tmax) {
-  return TileShape{tmax, kNW}.lds_bytes() + 32 * tmax * (int64_t)sizeof(int);
-}
-
-// 32-row parts of the largest tile, and the most tiles that the pairs can form.
-int tile_parts(const GroupedShape&) { return 4; }
-int64_t most_tiles(const GroupedShape& g) {
-  return g.P / (32 * tile_parts(g)) + (g.E < g.P ? g.E : g.P);
-}
-
-template <int TMAX, int EPI>
+template <class F, int EPI>
 hipError_t launch_t(const void* q8, const int* groups, const void* w, float* out,
                     const GroupedShape& g, const Epilogue& epi, hipStream_t s) {
   const uint8_t* base = static_cast<const uint8_t*>(q8);
-  auto kern = grouped_kernel<TMAX, EPI>;
-  constexpr int64_t lds = lds_bytes(TMAX);
-  if (lds > 65536) {
+  auto kern = grouped_kernel<F, EPI>;
+  if (F::kLds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, F::kLds);
     if (e != hipSuccess) return e;
   }
-  const int64_t gn = (g.N + 32 * kNW - 1) / (32 * kNW);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grouped_grid(g)), dim3(64 * kNW), (size_t)lds, s,
-                     reinterpret_cast<const int8_t*>(base),
-                     reinterpret_cast<const float*>(base + q8_planes_offset(g.q_rows, g.K)),
-                     reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(g.q_rows, g.K)),
-                     groups, static_cast<const uint8_t*>(w), out, (int)g.P, (int)g.E, (int)g.N,
-                     (int)g.K, (int)g.q_rows, (int)g.per_row, (int)gn, (int)most_tiles(g),
-                     (int)GroupLayout{g.P, g.E}.order(), epi_param<EPI>(epi));
+  const int64_t gn = ((g.N + 31) / 32 + F::CW - 1) / F::CW;
+  const int64_t most = g.P / F::BM + (g.E < g.P ? g.E : g.P);
+  const int64_t grid = (most * gn + 7) / 8 * 8;
+  const Args a{reinterpret_cast<const int8_t*>(base),
+               reinterpret_cast<const float*>(base + q8_planes_offset(g.q_rows, g.K)),
+               reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(g.q_rows, g.K)),
+               groups, static_cast<const uint8_t*>(w), out, (int)g.P, (int)g.E, (int)g.N, (int)g.K,
+               (int)g.q_rows, (int)g.per_row, (int)gn, (int)GroupLayout{g.P, g.E}.order(),
+               (int)most};
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * F::NW), (size_t)F::kLds, s, a,
+                     epi_param<EPI>(epi));
   return hipGetLastError();
 }
 
+// The forms of the kernel, and what a workgroup of each takes: fixed microseconds, and per super-block.
+using Wide = Form<4, 8, 1, 2>;   // 128 rows x 256 weight rows, one workgroup to a compute unit
+using Narrow = Form<1, 4, 1, 4>; // 32 x 128, four
+using Split2 = Form<1, 4, 2, 4>; // 32 x 128, K in two ranges, two
+using Split4 = Form<1, 4, 4, 4>; // 32 x 128, K in four ranges, one
+
 template <int EPI>
 hipError_t launch_epi(const void* q8, const int* groups, const void* w, float* out,
-                      const GroupedShape& g, const Epilogue& epi, hipStream_t s) {
-  return launch_t<4, EPI>(q8, groups, w, out, g, epi, s);
+                      const GroupedShape& g, const Epilogue& epi, int64_t cus, hipStream_t s) {
+  switch (grouped_form(g, cus)) {
+    case kGroupedNarrow: return launch_t<Narrow, EPI>(q8, groups, w, out, g, epi, s);
+    case kGroupedSplit2: return launch_t<Split2, EPI>(q8, groups, w, out, g, epi, s);
+    case kGroupedSplit4: return launch_t<Split4, EPI>(q8, groups, w, out, g, epi, s);
+    default: return launch_t<Wide, EPI>(q8, groups, w, out, g, epi, s);
+  }
 }
 
 }  // namespace
 
-int64_t grouped_grid(const GroupedShape& g) {
-  const int64_t gn = (g.N + 32 * kNW - 1) / (32 * kNW);
-  return (most_tiles(g) * gn + 7) / 8 * 8;
+GroupedForm grouped_form(const GroupedShape& g, int64_t compute_units) {
+  const double cus = (double)compute_units, nsb = (double)(g.K / 256);
+  const double ntiles = (double)((g.N + 31) / 32);
+  // experts that P evenly drawn pairs name, and the tiles of 32 and 128 rows they make
+  const double E = (double)g.E, P = (double)g.P;
+  const double used = E * (1.0 - std::pow(1.0 - 1.0 / E, P)), r = P / used;
+  const double t32 = used * std::max(1.0, r / 32.0 + 0.5);
+  const double t128 = used * std::max(1.0, r / 128.0 + 0.5);
+  // rounds of a grid over the device: one, or, the last one being partly empty, half a round more
+  auto rounds = [](double grid, double slots) { return grid <= slots ? 1.0 : grid / slots + 0.5; };
+  // per super-block of a 32-row tile with u wavefronts to a SIMD
+  auto us = [](double u) {
+    return u <= 2.0 ? 1.5 + 0.3 * std::max(u, 1.0) : u <= 4.0 ? 2.1 + 0.55 * (u - 2.0) : 3.2;
+  };
+  const double wide = t128 * std::ceil(ntiles / 8.0), narrow = t32 * std::ceil(ntiles / 4.0);
+  const double load = narrow / cus;
+  const double cost[4] = {
+      rounds(wide, cus) * (nsb * (1.0 + 0.95 * t32 / t128) + 13.0),
+      rounds(narrow, 4.0 * cus) * (nsb * us(load) + 5.0),
+      rounds(narrow, 2.0 * cus) * (std::ceil(nsb / 2.0) * us(2.0 * load) + 6.0),
+      rounds(narrow, cus) * (std::ceil(nsb / 4.0) * 3.5 + 7.0)};
+  return (GroupedForm)(std::min_element(cost, cost + 4) - cost);
 }
-int64_t grouped_lds_bytes(const GroupedShape& g) { return lds_bytes(tile_parts(g)); }
+
+int64_t grouped_lds_bytes(GroupedForm f) {
+  return f == kGroupedNarrow   ? Narrow::kLds
+         : f == kGroupedSplit2 ? Split2::kLds
+         : f == kGroupedSplit4 ? Split4::kLds
+                               : Wide::kLds;
+}
 
 hipError_t launch_grouped(const void* q8, const int* groups, const void* w, float* out,
-                          const GroupedShape& g, const Epilogue& epi, hipStream_t s) {
-  return epi.kind == kEpiGated ? launch_epi<kEpiGated>(q8, groups, w, out, g, epi, s)
-                               : launch_epi<kEpiAct>(q8, groups, w, out, g, epi, s);
+                          const GroupedShape& g, const Epilogue& epi, int64_t cus, hipStream_t s) {
+  return epi.kind == kEpiGated ? launch_epi<kEpiGated>(q8, groups, w, out, g, epi, cus, s)
+                               : launch_epi<kEpiAct>(q8, groups, w, out, g, epi, cus, s);
 }
 
 }  // namespace mmq

@@ -64,12 +64,12 @@ int check_act(int32_t act) {
              : MMQ_OK;
 }
 
-// The device, and that the product's kernel fits its LDS.
-int check_device(const GroupedShape& g) {
-  int64_t budget = 0, cus = 0;
-  const int st = mmq::api_current_device(&budget, &cus);
+// The device's compute units, and that the product's kernel fits its LDS.
+int check_device(const GroupedShape& g, int64_t* cus) {
+  int64_t budget = 0;
+  const int st = mmq::api_current_device(&budget, cus);
   if (st) return st;
-  const int64_t need = mmq::grouped_lds_bytes(g);
+  const int64_t need = mmq::grouped_lds_bytes(mmq::grouped_form(g, *cus));
   if (need > budget)
     return fail(MMQ_E_LDS, "the grouped product needs %lld bytes of LDS, the device allows %lld",
                 (long long)need, (long long)budget);
@@ -135,30 +135,31 @@ LayerSpace layer_space(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F) {
 }
 
 hipError_t run_product(const GroupedShape& g, const float* x, const int32_t* groups, const void* w,
-                       float* out, void* q8, const mmq::Epilogue& epi, hipStream_t s) {
+                       float* out, void* q8, const mmq::Epilogue& epi, int64_t cus,
+                       hipStream_t s) {
   const hipError_t e = mmq::launch_quantize_rows(x, g.q_rows, g.K, q8, s);
-  return e != hipSuccess ? e : mmq::launch_grouped(q8, groups, w, out, g, epi, s);
+  return e != hipSuccess ? e : mmq::launch_grouped(q8, groups, w, out, g, epi, cus, s);
 }
 
 hipError_t run_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, const float* x,
                      const int32_t* groups, const void* w, float* H, void* q8, int32_t act,
-                     hipStream_t s) {
+                     int64_t cus, hipStream_t s) {
   mmq::Epilogue epi;
   epi.kind = mmq::kEpiGated;
   epi.act = act;
   epi.F = F;
-  return run_product(gated_shape(M, E, k, F, D), x, groups, w, H, q8, epi, s);
+  return run_product(gated_shape(M, E, k, F, D), x, groups, w, H, q8, epi, cus, s);
 }
 
 hipError_t run_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, const float* H,
                     const int32_t* groups, const float* weights, const void* w,
-                    const float* residual, float* out, void* workspace, hipStream_t s) {
+                    const float* residual, float* out, void* workspace, int64_t cus, hipStream_t s) {
   const DownSpace sp = down_space(M, k, D, F);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* Y = reinterpret_cast<float*>(ws + sp.Y);
   mmq::Epilogue epi;
   epi.kind = mmq::kEpiAct;
-  const hipError_t e = run_product(down_shape(M, E, k, D, F), H, groups, w, Y, ws + sp.q8, epi, s);
+  const hipError_t e = run_product(down_shape(M, E, k, D, F), H, groups, w, Y, ws + sp.q8, epi, cus, s);
   if (e != hipSuccess) return e;
   return mmq::launch_combine(Y, groups + GroupLayout{M * k, E}.place(), weights, residual, out, M, k,
                              D, s);
@@ -204,11 +205,12 @@ int mmq_q4K_grouped(int64_t M, int64_t E, int64_t k, int64_t N, int64_t K, const
   if (!st) st = check_pointers({x, groups, w_rep, C, q8});
   if (st) return st;
   const GroupedShape g{M * k, E, N, K, rows, per_pair ? 1 : k};
-  if ((st = check_device(g))) return st;
+  int64_t cus = 0;
+  if ((st = check_device(g, &cus))) return st;
   mmq::Epilogue epi;
   epi.kind = mmq::kEpiAct;
   epi.act = act;
-  return hip_status("mmq_q4K_grouped", run_product(g, x, groups, w_rep, C, q8, epi,
+  return hip_status("mmq_q4K_grouped", run_product(g, x, groups, w_rep, C, q8, epi, cus,
                                                    static_cast<hipStream_t>(stream)));
 }
 
@@ -217,10 +219,11 @@ int mmq_q4K_grouped_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D,
                           int32_t act, void* stream) {
   int st = check_gated(M, E, k, F, D, act);
   if (!st) st = check_pointers({x, groups, w_pairs, H, q8});
-  if (!st) st = check_device(gated_shape(M, E, k, F, D));
+  int64_t cus = 0;
+  if (!st) st = check_device(gated_shape(M, E, k, F, D), &cus);
   if (st) return st;
   return hip_status("mmq_q4K_grouped_gated",
-                    run_gated(M, E, k, F, D, x, groups, w_pairs, H, q8, act,
+                    run_gated(M, E, k, F, D, x, groups, w_pairs, H, q8, act, cus,
                               static_cast<hipStream_t>(stream)));
 }
 
@@ -240,10 +243,11 @@ int mmq_q4K_grouped_down(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, 
   int st = check_down(M, E, k, D, F);
   if (!st) st = check_pointers({H, groups, weights, w_down, out, workspace}, residual);
   if (!st) st = check_bytes(workspace_bytes, down_space(M, k, D, F).total);
-  if (!st) st = check_device(down_shape(M, E, k, D, F));
+  int64_t cus = 0;
+  if (!st) st = check_device(down_shape(M, E, k, D, F), &cus);
   if (st) return st;
   return hip_status("mmq_q4K_grouped_down",
-                    run_down(M, E, k, D, F, H, groups, weights, w_down, residual, out, workspace,
+                    run_down(M, E, k, D, F, H, groups, weights, w_down, residual, out, workspace, cus,
                              static_cast<hipStream_t>(stream)));
 }
 
@@ -270,8 +274,9 @@ int mmq_q4K_grouped_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, c
   if (st) return st;
   const LayerSpace w = layer_space(M, E, k, D, F);
   if ((st = check_bytes(workspace_bytes, w.total))) return st;
-  if ((st = check_device(gated_shape(M, E, k, F, D)))) return st;
-  if ((st = check_device(down_shape(M, E, k, D, F)))) return st;
+  int64_t cus = 0;
+  if ((st = check_device(gated_shape(M, E, k, F, D), &cus))) return st;
+  if ((st = check_device(down_shape(M, E, k, D, F), &cus))) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   int* ids = reinterpret_cast<int*>(ws + w.ids);
   float* weights = reinterpret_cast<float*>(ws + w.weights);
@@ -280,9 +285,9 @@ int mmq_q4K_grouped_moe(int64_t M, int64_t E, int64_t k, int64_t D, int64_t F, c
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = mmq::launch_moe_route(logits, M, E, k, score, renorm, ids, weights, nullptr, s);
   if (e == hipSuccess) e = mmq::launch_group(ids, M * k, E, groups, s);
-  if (e == hipSuccess) e = run_gated(M, E, k, F, D, x, groups, w_pairs, H, ws + w.down, act, s);
+  if (e == hipSuccess) e = run_gated(M, E, k, F, D, x, groups, w_pairs, H, ws + w.down, act, cus, s);
   if (e == hipSuccess)
-    e = run_down(M, E, k, D, F, H, groups, weights, w_down, residual, out, ws + w.down, s);
+    e = run_down(M, E, k, D, F, H, groups, weights, w_down, residual, out, ws + w.down, cus, s);
   return hip_status("mmq_q4K_grouped_moe", e);
 }
 

@@ -36,14 +36,17 @@ hipError_t launch_group(const int* ids, int64_t P, int64_t E, int* groups, hipSt
 struct GroupedShape {
   int64_t P, E, N, K, q_rows, per_row;
 };
-// Workgroups of the product's grid.
-int64_t grouped_grid(const GroupedShape& g);
-int64_t grouped_lds_bytes(const GroupedShape& g);
+// The kernel's form for a shape, chosen by a cost model (grouped.hip) as if the pairs fell evenly on
+// the experts, and its LDS.
+enum GroupedForm { kGroupedWide, kGroupedNarrow, kGroupedSplit2, kGroupedSplit4 };
+GroupedForm grouped_form(const GroupedShape& g, int64_t compute_units);
+int64_t grouped_lds_bytes(GroupedForm f);
 // The q8 buffer is quantize_q8_1's but for its float pairs, which are [M][K/32] here (row by row,
 // so that the rows of a group can be gathered); K % 256 == 0.
 hipError_t launch_quantize_rows(const float* x, int64_t M, int64_t K, void* q8, hipStream_t s);
 hipError_t launch_grouped(const void* q8, const int* groups, const void* w, float* out,
-                          const GroupedShape& g, const Epilogue& epi, hipStream_t s);
+                          const GroupedShape& g, const Epilogue& epi, int64_t compute_units,
+                          hipStream_t s);
 
 // out[t][D] = residual[t] + sum over s of weights[t][s] * Y[t*k + s], over the pairs with an expert.
 hipError_t launch_combine(const float* Y, const int* place, const float* weights,

@@ -1,6 +1,7 @@
-"""The products grouped by expert on the GPU: the sort of the pairs, the grouped product and its gated
-form bit for bit against the plain product of each expert's rows, the weighted sum and the whole layer
-against the float64 oracle, in graphs, on two streams, and with groups of nonsense.
+"""The products grouped by expert on the GPU: the sort of the pairs, the grouped product, its gated form
+and the weighted sum against the float64 oracle, the unsplit forms of the kernel bit for bit against the
+plain product of each expert's rows, the whole layer against its calls, in graphs, on two streams, and
+groups of nonsense.
 """
 import functools
 
@@ -9,6 +10,7 @@ import pytest
 
 import synth
 from oracle import layer_oracle as lo
+from tests import grouped_util as gu
 from tests import layer_util as lu
 from tests.gpu_util import say, to_dev
 
@@ -127,8 +129,9 @@ def ragged_ids(counts, k, rng, none=3):
 
 
 def plain_rows(x, rep, e, n_bytes, N, K):
-    """The plain product of some rows with expert e's matrix, by a tile that the grouped one shares its
-    order of additions with (the decode and skinny tiles, which few rows get by default, have others)."""
+    """The plain product of some rows with expert e's matrix, by a tile that the unsplit grouped forms
+    share their order of additions with (the decode and skinny tiles, which few rows get by default,
+    have others)."""
     M = x.shape[0]
     q8, C = raw(mmq.mmq_q8_1_bytes(M, K)), f32(M, N)
     mmq.quantize_q8_1(x, M, K, q8)
@@ -137,31 +140,68 @@ def plain_rows(x, rep, e, n_bytes, N, K):
     return C
 
 
+# one super-block, and more of them than ranges of K in each form, and than fit them evenly
 @pytest.mark.parametrize("per_pair", [False, True])
 @pytest.mark.parametrize("k,N,K", [(1, 64, 256), (2, 70, 512), (1, 258, 768), (3, 515, 1280),
-                                   (2, 1, 256), (1, 2050, 512)])
-def test_grouped_is_the_plain_product_of_each_expert(k, N, K, per_pair):
+                                   (2, 1, 256), (1, 2050, 512), (1, 130, 2816), (2, 33, 4096)])
+def test_grouped(k, N, K, per_pair):
     E = len(RAGGED)
-    rng = np.random.default_rng(N + K)
-    ids = ragged_ids(RAGGED, k, rng)
+    ids = ragged_ids(RAGGED, k, np.random.default_rng(N + K))
     M = ids.shape[0]
     rows = M * k if per_pair else M
-    x = to_dev(synth.activations("normal_outliers", rows, K, N))
-    rep, _, _ = experts("plain", E, N, K, 40)
-    n = mmq.mmq_q4K_repacked_bytes(N, K)
-    g = group(ids, E)
+    xh = synth.activations("normal_outliers", rows, K, N)
+    rep, ws, _ = experts("plain", E, N, K, 40)
     q8, C = raw(mmq.mmq_q8_1_bytes(rows, K)), f32(M * k, N)
-    say("grouped", (M, E, k, N, K), "per pair" if per_pair else "per token")
-    mmq.mmq_q4K_grouped(M, E, k, N, K, x, g, rep, C, q8, per_pair=per_pair)
+    say("grouped", (M, E, k, N, K), "per pair" if per_pair else "per token",
+        gu.grouped_form(M * k, E, N, K))
+    mmq.mmq_q4K_grouped(M, E, k, N, K, to_dev(xh), group(ids, E), rep, C, q8, per_pair=per_pair)
     got = host(C)
     flat = ids.reshape(-1)
     assert np.all(np.isnan(got[(flat < 0) | (flat >= E)])), "rows without an expert were written"
     for e in range(E):
         ps = np.nonzero(flat == e)[0]
         if ps.size:
-            src = torch.from_numpy(ps if per_pair else ps // k).cuda()
-            want = host(plain_rows(x[src].contiguous(), rep, e, n, N, K))
-            assert np.array_equal(got[ps], want), e
+            P, T = lu.product(np.ascontiguousarray(xh[ps if per_pair else ps // k]), ws[e])
+            lu.assert_close(got[ps], P, lu.BAR * T, what=f"expert {e}")
+
+
+# few experts with few rows (every form in turn as the grid shrinks); the last one: many rows
+FORMS = [("narrow", 200, 8, 2, 8200, 768), ("split2", 200, 8, 2, 2050, 2048),
+         ("split4", 300, 8, 2, 1290, 4352), ("wide", 4096, 4, 2, 2050, 2048)]
+
+
+@pytest.mark.parametrize("form,M,E,k,N,K", FORMS)
+def test_every_form(form, M, E, k, N, K):
+    """Each form of the kernel, on ragged experts, against the plain product of each expert's rows: bit
+    for bit where K is not split, else within both products' bars."""
+    assert gu.grouped_form(M * k, E, N, K) == form
+    rng = np.random.default_rng(M)
+    ids = np.minimum(rng.geometric(0.3, (M, k)) - 1, E).astype(np.int32)   # E: none
+    x = to_dev(synth.activations("normal_outliers", M, K, N))
+    blocks = synth.q4k_weights("random_fields", E * N, K, 3)[0]
+    n = mmq.mmq_q4K_repacked_bytes(N, K)
+    rep = raw(E * n)
+    for e in range(E):
+        mmq.repack_q4_K(to_dev(blocks[e * N:(e + 1) * N]), N, K, rep[e * n:(e + 1) * n])
+    C, q8 = f32(M * k, N), raw(mmq.mmq_q8_1_bytes(M, K))
+    say("grouped", form, (M, E, k, N, K))
+    mmq.mmq_q4K_grouped(M, E, k, N, K, x, group(ids, E), rep, C, q8)
+    flat = ids.reshape(-1)
+    for e in range(E):
+        ps = torch.from_numpy(np.nonzero(flat == e)[0]).cuda()
+        if not ps.numel():
+            continue
+        want, got = plain_rows(x[ps // k].contiguous(), rep, e, n, N, K), C[ps]
+        if form in ("wide", "narrow"):
+            assert torch.equal(got, want), e
+        else:
+            some = np.arange(min(len(ps), 20))
+            _, T = lu.product(np.ascontiguousarray(host(x[ps[:20] // k])),
+                              blocks[e * N:(e + 1) * N])
+            lu.assert_close(host(got)[some], host(want)[some].astype(np.float64), 2 * lu.BAR * T)
+            # and every row to a looser bound of the whole: a row that is wrong is far off
+            assert float((got - want).abs().max()) <= 1e-4 * float(want.abs().max())
+    assert bool(torch.isnan(C[torch.from_numpy(np.nonzero(flat == E)[0]).cuda()]).all())
 
 
 @pytest.mark.parametrize("act", lo.ACTS)
@@ -185,29 +225,47 @@ def test_grouped_activation(act):
 
 
 @pytest.mark.parametrize("k,F,D", [(1, 64, 256), (2, 40, 512), (1, 129, 768), (3, 515, 1280),
-                                   (2, 1, 256), (1, 1030, 256)])
-def test_grouped_gated_is_the_gated_product_of_each_expert(k, F, D):
+                                   (2, 1, 256), (1, 1030, 256), (2, 17, 4096)])
+def test_grouped_gated(k, F, D):
     E = len(RAGGED)
     ids = ragged_ids(RAGGED, k, np.random.default_rng(F + D))
     M = ids.shape[0]
-    x = to_dev(synth.activations("normal_outliers", M, D, F))
-    rep, _, _ = experts("pair", E, F, D, 300)
-    n = mmq.mmq_q4K_pair_bytes(F, D)
+    xh = synth.activations("normal_outliers", M, D, F)
+    rep, gate, up = experts("pair", E, F, D, 300)
     q8, H = raw(mmq.mmq_q8_1_bytes(M, D)), f32(M * k, F)
-    say("grouped gated", (M, E, k, F, D))
-    mmq.mmq_q4K_grouped_gated(M, E, k, F, D, x, group(ids, E), rep, H, q8, act=mmq.MMQ_ACT_SILU)
+    say("grouped gated", (M, E, k, F, D), gu.grouped_form(M * k, E, -(-F // 16) * 32, D))
+    mmq.mmq_q4K_grouped_gated(M, E, k, F, D, to_dev(xh), group(ids, E), rep, H, q8,
+                              act=mmq.MMQ_ACT_SILU)
     got, flat = host(H), ids.reshape(-1)
-    assert np.all(np.isnan(got[(flat < 0) | (flat >= E)])), "rows without an expert were written"
-    for e in range(E):
-        ps = np.nonzero(flat == e)[0]
-        if not ps.size:
-            continue
-        rows = x[torch.from_numpy(ps // k).cuda()].contiguous()
-        qe, He = raw(mmq.mmq_q8_1_bytes(ps.size, D)), f32(ps.size, F)
-        mmq.quantize_q8_1(rows, ps.size, D, qe)
-        mmq.mmq_q4K_q8_1_gated(ps.size, F, D, qe, rep[e * n:(e + 1) * n], He,
-                               act=mmq.MMQ_ACT_SILU, force_tile=mmq.MMQ_TILE_LARGE)
-        assert np.array_equal(got[ps], host(He)), e
+    none = (flat < 0) | (flat >= E)
+    assert np.all(np.isnan(got[none])), "rows without an expert were written"
+    want, err = lu.experts_gated(xh, ids, gate, up, "silu")
+    lu.assert_close(got[~none], want[~none], err[~none])
+
+
+def test_grouped_gated_is_the_gated_product_of_each_expert():
+    """Bit for bit, in the unsplit forms."""
+    for form, M, E, k, F, D in (("narrow", 300, 6, 2, 4100, 256), ("wide", 2048, 2, 2, 2050, 2048)):
+        assert gu.grouped_form(M * k, E, -(-F // 16) * 32, D) == form
+        ids = np.random.default_rng(F).integers(0, E, (M, k)).astype(np.int32)
+        x = to_dev(synth.activations("normal_outliers", M, D, F))
+        n, m = mmq.mmq_q4K_pair_bytes(F, D), F * (D // 256) * 144
+        blocks = to_dev(synth.q4k_weights("random_fields", 2 * E * F, D, 5)[0]).reshape(2 * E, -1)
+        rep = raw(E * n)
+        for e in range(E):
+            mmq.repack_q4_K_pair(blocks[e], blocks[E + e], F, D, rep[e * n:(e + 1) * n])
+        H = f32(M * k, F)
+        say("grouped gated", form, (M, E, k, F, D))
+        mmq.mmq_q4K_grouped_gated(M, E, k, F, D, x, group(ids, E), rep, H,
+                                  raw(mmq.mmq_q8_1_bytes(M, D)), act=mmq.MMQ_ACT_GELU)
+        for e in range(E):
+            ps = torch.from_numpy(np.nonzero(ids.reshape(-1) == e)[0]).cuda()
+            rows, He = x[ps // k].contiguous(), f32(ps.numel(), F)
+            qe = raw(mmq.mmq_q8_1_bytes(ps.numel(), D))
+            mmq.quantize_q8_1(rows, ps.numel(), D, qe)
+            mmq.mmq_q4K_q8_1_gated(ps.numel(), F, D, qe, rep[e * n:(e + 1) * n], He,
+                                   act=mmq.MMQ_ACT_GELU, force_tile=mmq.MMQ_TILE_LARGE)
+            assert torch.equal(H[ps], He), (form, e)
 
 
 # few and many rows per expert, experts that no one names, one expert that everyone names, tokens
