@@ -13,9 +13,9 @@ def values(w):
     return v
 
 
-def product(x, w, scales, zeros, group: int):
-    """(x w^T, T) float64 [M, N]; T = sum_k |x s| (v + |z|), the absolute values of the terms that the
-    sums are made of: sum x v and z sum x, scaled."""
+def product(x, w, scales, zeros, group: int, offset: float = 0.0):
+    """(x w^T, T) float64 [M, N]; T = sum_k |x s| (offset + v + |offset + z|), the absolute values of the
+    terms that a sum is made of which takes s (sum x (offset + v) - (offset + z) sum x)."""
     x = np.asarray(x, np.float64)
     v = values(w)
     M, K = x.shape
@@ -25,14 +25,14 @@ def product(x, w, scales, zeros, group: int):
         z = 8.0 if zeros is None else np.asarray(zeros, np.float64)[:, g:g + 1]
         part, vg = x[:, k0:k0 + group], v[:, k0:k0 + group]
         y += (part @ (vg - z).T) * s
-        T += (np.abs(part) @ (vg + np.abs(z)).T) * np.abs(s)
+        T += (np.abs(part) @ (offset + vg + np.abs(offset + z)).T) * np.abs(s)
     return y, T
 
 
 def bound(T, K: int):
     """How far a float32 evaluation may be off. A result's longest chain of additions: the 128 products
     of a record on the matrix unit, whose additions are taken to be good to a whole unit in the last
-    place (2^-23), the zero and the scale, at most 4 folds for each of the K/128 records, 16
-    wavefronts and 3 pieces, half a unit (2^-24) each."""
+    place (2^-23), 3 pieces, the zero and the scale, at most 4 folds for each of the K/128 records and 16
+    wavefronts, half a unit (2^-24) each."""
     records = -(-K // 128)
     return (2 * 128 + 2 + 4 * records + 16 + 3) * 2.0 ** -24 * T

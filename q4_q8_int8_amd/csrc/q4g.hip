@@ -3,21 +3,25 @@
 //
 //   y[i][j] = act( sum_g s_jg ( sum_{k in g} x_ik v_jk - z_jg sum_{k in g} x_ik ) + bias_j ) + res_ij
 //
-// The nibbles v are exact in f16 and bf16, and so is every product x v in float32, so the inner sums
-// run on v_mfma_f32_16x16x32_{f16,bf16} with float32 accumulators: 16 weight rows (src0) by 16
-// columns (src1). A float16 or bfloat16 token is one column. A float32 token is three: its values'
-// three bf16 pieces, which sum to them exactly (bf16_trunc3), so nothing is rounded before the
-// float32 sums, whatever the type. sum x is the same instruction with a row of ones, and lands where
-// the fold needs it. The zero stays out of the operand (a zero need not be a whole number) and costs
-// two FMAs per group and result.
+// The inner sums run on v_mfma_f32_16x16x32_{f16,bf16} with float32 accumulators: src0 has 16 columns
+// of activations, src1 16 weight rows, so a lane's four results are of one weight row and share its
+// scale. Every product is exact in float32: a nibble is exact in f16; for bf16 the operand is 16 + v
+// (the bits of 16 with v in the upper mantissa bits, one AND-OR behind a shift), and the 16 goes out
+// with the zero, - (16 + z) sum x. A float16 or bfloat16 token is one column, token t being column
+// 4 (t % 4) + t / 4, so that up to four tokens need one result register. A float32 token is three
+// columns, its values' three bf16 pieces, which sum to them exactly (bf16_trunc3): token t has columns
+// 4 (t % 4) .. + 2 of column tile t / 4, so that its three sums meet in one lane. sum x is the same
+// instruction with ones for weights; the matrix unit is idle most of the time.
 //
-// Bound by the bytes of the weights: a workgroup has 16 rows, its wavefronts take the records of 128
-// values in turn (so that together they stream contiguous memory), load kBatch of them ahead, and
-// add their sums through LDS in the order of the wavefronts. The matrix instructions are idle most
-// of the time with few tokens; what counts beside the loads is unpacking: 9 vector instructions per
-// 8 values to f16 (or the exponent of 1024 over the nibble, subtract 1024), 15 to bf16 (convert
-// bytes to float32, keep the high halves).
-#include <type_traits>
+// Bound by the bytes of the weights. A workgroup, one to a compute unit, works through tiles of 16 rows; its
+// wavefronts take the records of 128 values in turn (together they stream contiguous memory), each with
+// kAhead records in flight, across the tiles too. Their sums of several tiles are added together, through
+// LDS, in the order of the wavefronts: a barrier for every tile costs as much as a tile's loads. A
+// wavefront brings the values of x for its own records into LDS with its first tile, in the form of the
+// operands: read from memory for every tile they take more of the vector memory unit than the weights do,
+// and their latency is not covered. Beside the loads, unpacking counts: 9 vector instructions per 8 values
+// for f16 and 8 for bf16.
+#include <algorithm>
 
 #include "epilogue.h"
 #include "mmq_device.h"
@@ -31,57 +35,94 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-constexpr int kBatch = 2;                 // records a wavefront loads ahead
-constexpr int kPitch = kG4Values * 2 + 16;  // LDS bytes per column of pieces: 16-byte reads spread
+constexpr int kAhead = 4;              // records of a wavefront in flight, per tile
+constexpr int kRowBytes = kG4Values * 2;  // LDS bytes of a row of a record's operands
+// Wavefronts of a workgroup at most: the sums of many float32 tokens take registers.
+constexpr int max_waves(int x_type, int q) { return x_type == kTypeF32 && q > 1 ? 8 : 16; }
+// The rows of x in LDS: of each token one, or three of pieces.
+__host__ __device__ constexpr int x_rows(int x_type, int64_t M) {
+  return (int)(x_type == kTypeF32 ? 3 * M : M);
+}
+// Where the 16 bytes `part` (0..15) of a row are: moved about by the row, so that the same part of
+// neighbouring rows is in different banks.
+__device__ __forceinline__ int x_place(int row, int part) {
+  return row * kRowBytes + ((part ^ (row & 15)) * 16);
+}
 
-// Columns of 16 that M tokens make.
-constexpr int columns(int x_type, int64_t M) { return (int)(x_type == kTypeF32 ? 3 * M : M); }
-constexpr int column_tiles(int x_type, int64_t M) { return (columns(x_type, M) + 15) / 16; }
+// 16 bytes at a lane's offset from a wavefront's.
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_at, at, 0));
+}
 
-// The eight values of a dword as the matrix operand, four registers of two.
+// Constants that stay in vector registers, where an AND-OR can take them beside a mask in scalar ones (the
+// compiler would otherwise spend two instructions with literals).
+__device__ __forceinline__ uint32_t keep(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// The eight values of a dword as the matrix operand, four registers of two: v for f16, 16 + v for bf16.
 template <bool BF>
-__device__ __forceinline__ v4u unpack(uint32_t w) {
-  v4u o;
-  if constexpr (BF) {
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // nibbles j and j + 4
-      const uint32_t b = j & 1 ? hi : lo;
-      const int at = 8 * (j >> 1);
-      const float a = (float)((b >> at) & 0xFFu), c = (float)((b >> (at + 16)) & 0xFFu);
-      o[j] = pack_hi16(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, c));
-    }
-  } else {
-    // 0x6400 | v is 1024 + v and 0x5400 | v << 4 is 64 + v, exactly
-    const uint32_t w8 = w >> 8;
-    const v2h big = {(_Float16)1024.0f, (_Float16)1024.0f}, mid = {(_Float16)64.0f, (_Float16)64.0f};
-    const uint32_t p[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x54005400u,
-                           (w8 & 0x000F000Fu) | 0x64006400u, (w8 & 0x00F000F0u) | 0x54005400u};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, p[j]) - (j & 1 ? mid : big));
+struct Unpack;
+template <>
+struct Unpack<true> {
+  uint32_t sixteen = keep(0x41804180u);
+  __device__ __forceinline__ v4u operator()(uint32_t w) const {
+    constexpr uint32_t mask = 0x00780078u;
+    return v4u{((w << 3) & mask) | sixteen, ((w >> 1) & mask) | sixteen,
+               ((w >> 5) & mask) | sixteen, ((w >> 9) & mask) | sixteen};
   }
-  return o;
-}
+};
+template <>
+struct Unpack<false> {
+  // 0x6400 | v is 1024 + v and 0x5400 | v << 4 is 64 + v, exactly
+  uint32_t big = keep(0x64006400u), mid = keep(0x54005400u);
+  __device__ __forceinline__ v4u operator()(uint32_t w) const {
+    constexpr uint32_t low = 0x000F000Fu, high = 0x00F000F0u;
+    const uint32_t w8 = w >> 8;
+    return v4u{less((w & low) | big, big), less((w & high) | mid, mid),
+               less((w8 & low) | big, big), less((w8 & high) | mid, mid)};
+  }
+  static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, a) - __builtin_bit_cast(v2h, b));
+  }
+};
 
 template <bool BF>
-__device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+__device__ __forceinline__ v4f mfma(v4u x, v4u w, v4f c) {
   if constexpr (BF)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
-                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x),
+                                                   __builtin_bit_cast(v8bf, w), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
-                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x),
+                                                  __builtin_bit_cast(v8h, w), c, 0, 0, 0);
 }
 
-template <bool SBF>
-__device__ __forceinline__ float scale_of(uint2 u, int r) {
-  const uint32_t w = r & 2 ? u.y : u.x;
-  if constexpr (SBF)
-    return __builtin_bit_cast(float, r & 1 ? w & 0xFFFF0000u : w << 16);
-  else
-    return (float)__builtin_bit_cast(_Float16, (uint16_t)(r & 1 ? w >> 16 : w));
-}
+// A lane's S scales (or zeros) of a record, and the i-th of them.
+template <int S>
+struct Scales {
+  uint32_t u[S == 4 ? 2 : 1];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    if constexpr (S == 4) {
+      const uint2 v =
+          __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0));
+      u[0] = v.x;
+      u[1] = v.y;
+    } else if constexpr (S == 2) {
+      u[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0);
+    } else {
+      u[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, lane_at, at, 0);
+    }
+  }
+  template <bool BF>
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = u[i >> 1];
+    if constexpr (BF)
+      return __builtin_bit_cast(float, i & 1 ? w & 0xFFFF0000u : w << 16);
+    else
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+  }
+};
 
 __device__ __forceinline__ float load_as_float(const void* p, size_t i, int type) {
   if (type == kTypeF32) return static_cast<const float*>(p)[i];
@@ -94,184 +135,284 @@ __device__ __forceinline__ void store_float(void* p, size_t i, int type, float v
   else static_cast<__bf16*>(p)[i] = (__bf16)v;
 }
 
-// XT: the tokens' type. CT: column tiles. FOLDS: folds of a record, 1 where its 128 values lie in one
-// group, else 4, one per 32 values. SBF: bf16 scales.
-template <int XT, int CT, int FOLDS, bool ZEROS, bool SBF, int NW>
-__global__ __launch_bounds__(64 * NW) void q4g_kernel(const void* __restrict__ x,
-                                                      const uint8_t* __restrict__ rep, void* y,
-                                                      int y_type, int M, int N, int K, int group,
-                                                      size_t scales_at, size_t zeros_at,
-                                                      Q4GEpilogue epi) {
+// XT: the tokens' type. Q: groups of four tokens: column tiles for float32, else result registers. S:
+// scales of a row in a record. SBF: bf16 scales. ALL: x is in LDS for all records of a wavefront, else for
+// one, brought in anew for every record of every tile. The sums of `batch` tiles are added together.
+template <int XT, int Q, int S, bool SBF, bool ALL>
+__global__ __launch_bounds__(64 * max_waves(XT, Q)) void q4g_kernel(
+    const void* __restrict__ x, const uint8_t* __restrict__ rep, void* y, int y_type, int M, int N,
+    int K, int zeros, int batch, Q4GEpilogue epi) {
   constexpr bool F32 = XT == kTypeF32;
   constexpr bool BF = XT != kTypeF16;
+  constexpr int CT = F32 ? Q : 1;
+  constexpr bool PAIRS = F32 && Q == 1;
+  constexpr int XA = PAIRS ? 2 : 1;  // records whose x is in flight, in registers
   extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, threads = (int)blockDim.x;
+  const int nw = threads >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane >> 4, l16 = lane & 15;
-  const int tile = blockIdx.x;
-  const int nrec = (K + kG4Values - 1) / kG4Values;
-  const int ngroups = (K + group - 1) / group;
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(rep + (size_t)tile * nrec * kG4RecBytes, (uint32_t)nrec * kG4RecBytes);
-  const __amdgpu_buffer_rsrc_t rs =
-      make_rsrc(rep + scales_at + (size_t)tile * ngroups * 32, (uint32_t)ngroups * 32);
-  const __amdgpu_buffer_rsrc_t rz =
-      make_rsrc(rep + zeros_at + (size_t)tile * ngroups * 32, ZEROS ? (uint32_t)ngroups * 32 : 0u);
-  constexpr uint32_t XB = F32 ? 4 : 2;
-  const uint32_t x_bytes = (uint32_t)M * (uint32_t)K * XB;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(x, x_bytes);
+  const int ntiles = (N + kG4Rows - 1) / kG4Rows, nrec = (K + kG4Values - 1) / kG4Values;
+  // records of this wavefront in a tile
+  const int rounds = wave < nrec ? (nrec - wave + nw - 1) / nw : 0;
+  const int slots = ALL ? (nrec + nw - 1) / nw : 1;
+  const int rec_bytes = kG4ValueBytes + 32 * S * (zeros ? 2 : 1);
+  const uint32_t tile_bytes = (uint32_t)nrec * (uint32_t)rec_bytes;
+  const int grid = (int)gridDim.x;
 
-  struct Rec {
-    v4i w;
-    uint2 s[FOLDS], z[ZEROS ? FOLDS : 1];
-    v4u x[F32 ? 1 : 4];                      // 16-bit tokens: the operands of the four steps
-    float2 f[F32 ? (16 * CT + 2) / 3 : 1];   // float32: two values of each token
+  struct Weights {
+    v4i v;
+    Scales<S> s, z;
   };
-  constexpr int MT = F32 ? (16 * CT) / 3 : 0;  // float32 tokens that CT column tiles hold
-  auto load = [&](Rec& r, int rec) {
-    // past the last record every offset is past its buffer, and reads 0
-    const uint32_t o = (uint32_t)min(rec, nrec);
-    r.w = buf_load16_aux<kReadOnce>(rw, o * kG4RecBytes + lane * 16);
+  // record wave + j * nw of a tile
+  auto load_w = [&](Weights& r, int tile, int j) {
+    if (tile >= ntiles || j >= rounds) return;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(rep + (size_t)tile * tile_bytes, tile_bytes);
+    const int o = (wave + j * nw) * rec_bytes;
+    r.v = load16(rw, lane * 16, o);
+    r.s.load(rw, kG4ValueBytes + l16 * (2 * S), o);
+    if (zeros) r.z.load(rw, kG4ValueBytes + 32 * S + l16 * (2 * S), o);
+  };
+
+  // x of such a record, as the operands in this wavefront's LDS. Only it uses them, and its LDS operations
+  // are in order. 0 past K, where the operand of the weights need not be 0.
+  const int rows = x_rows(XT, M), row_bytes = rows * kRowBytes;
+  uint8_t* xw = smem + wave * (slots * row_bytes);
+  // 16-bit tokens go there by themselves, four tokens to an instruction: lane (c, l16) has the place l16 of
+  // token 4 q + c.
+  const uint32_t x_bytes = (uint32_t)M * (uint32_t)K * (F32 ? 4u : 2u);
+  const v4i rx = make_rsrc_sgpr(x, x_bytes);
+  const __amdgpu_buffer_rsrc_t rxb = make_rsrc(x, x_bytes);
+  const uint32_t xw_at = lds_addr(smem) + (uint32_t)(wave * (slots * row_bytes));
+  auto fetch_x = [&](int j, int slot) {
 #pragma unroll
-    for (int i = 0; i < FOLDS; ++i) {
-      const int k0 = (int)o * kG4Values + 32 * i;
-      const uint32_t at = k0 < K ? (uint32_t)(k0 / group) * 32u + c * 8 : 0x7FFFFFF0u;
-      r.s[i] = buf_load8_aux<0>(rs, at);
-      if constexpr (ZEROS) r.z[i] = buf_load8_aux<0>(rz, at);
+    for (int q = 0; q < Q; ++q) {
+      const int t = 4 * q + c, k = (wave + j * nw) * kG4Values + 8 * (l16 ^ (t & 15));
+      if (t < M)
+        dma16(rx, xw_at + (uint32_t)(slot * row_bytes + q * 4 * kRowBytes),
+              k < K ? ((uint32_t)t * (uint32_t)K + k) * 2u : x_bytes);
     }
-    if constexpr (F32) {
-      const uint32_t k = o * kG4Values + 2 * lane;
+  };
+  // float32 tokens through registers: up to four tokens two values of each to a lane, else 16 lanes to a
+  // token and eight values to a lane.
+  struct Tokens {
+    v4u a[PAIRS ? 1 : Q], b[PAIRS ? 1 : Q];
+    float2 f[PAIRS ? 4 : 1];
+  };
+  auto load_x = [&](Tokens& r, int j) {
+    if (j >= rounds) return;
+    if constexpr (PAIRS) {
+      const int k = (wave + j * nw) * kG4Values + 2 * lane;
+      const uint32_t at = k < K ? (uint32_t)k * 4u : x_bytes;
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        r.f[t] = t < M && (int)k < K
-                     ? buf_load_f32x2(rx, ((uint32_t)t * (uint32_t)K + k) * 4u)
-                     : make_float2(0.f, 0.f);
+      for (int t = 0; t < 4; ++t)
+        if (t < M) r.f[t] = buf_load_f32x2(rxb, at + (uint32_t)t * (uint32_t)K * 4u);
+    } else {
+      const int k = (wave + j * nw) * kG4Values + 8 * l16;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int t = 4 * q + c;
+        const uint32_t at = t < M && k < K ? ((uint32_t)t * (uint32_t)K + k) * 4u : x_bytes;
+        r.a[q] = __builtin_bit_cast(v4u, buf_load16(rxb, at));
+        r.b[q] = __builtin_bit_cast(v4u, buf_load16(rxb, at + 16));
+      }
+    }
+  };
+  auto put_x = [&](const Tokens& r, int slot) {
+    uint8_t* xj = xw + slot * row_bytes;
+    if constexpr (PAIRS) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= M) break;
+        uint32_t a[3], b[3];
+        bf16_trunc3(r.f[t].x, a[0], a[1], a[2]);
+        bf16_trunc3(r.f[t].y, b[0], b[1], b[2]);
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+          *reinterpret_cast<uint32_t*>(xj + x_place(3 * t + n, lane >> 2) + (lane & 3) * 4) =
+              pack_hi16(a[n], b[n]);
+      }
     } else {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const uint32_t k = o * kG4Values + 32 * m;
-        const uint32_t at = l16 < M && (int)k < K
-                                ? ((uint32_t)l16 * (uint32_t)K + k + 8 * c) * 2u
-                                : x_bytes;
-        r.x[m] = __builtin_bit_cast(v4u, buf_load16(rx, at));
-      }
-    }
-  };
-
-  v4f out[CT];
+      for (int q = 0; q < Q; ++q) {
+        const int t = 4 * q + c;
+        if (t >= M) continue;
+        uint32_t pc[8][3];
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct) out[ct] = v4f{0.f, 0.f, 0.f, 0.f};
-  const v4u ones = BF ? v4u{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
-                      : v4u{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-  uint8_t* cols = smem + wave * (16 * CT * kPitch);  // this wavefront's pieces, [column][128]
-
-  auto compute = [&](const Rec& r) {
-    if constexpr (F32) {
-      // the pieces of two values of each token; only this wavefront uses the region, and its LDS
-      // operations are in order, so the reads of the record before are done
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if (t < M) {
-          uint32_t a[3], b[3];
-          bf16_trunc3(r.f[t].x, a[0], a[1], a[2]);
-          bf16_trunc3(r.f[t].y, b[0], b[1], b[2]);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint32_t*>(cols + (3 * t + i) * kPitch + lane * 4) =
-                pack_hi16(a[i], b[i]);
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t bits = e < 4 ? r.a[q][e & 3] : r.b[q][e & 3];
+          bf16_trunc3(__builtin_bit_cast(float, bits), pc[e][0], pc[e][1], pc[e][2]);
         }
+#pragma unroll
+        for (int n = 0; n < 3; ++n)
+          *reinterpret_cast<v4u*>(xj + x_place(3 * t + n, l16)) =
+              v4u{pack_hi16(pc[0][n], pc[1][n]), pack_hi16(pc[2][n], pc[3][n]),
+                  pack_hi16(pc[4][n], pc[5][n]), pack_hi16(pc[6][n], pc[7][n])};
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  // This lane's column: of a 16-bit token, or a piece of a float32 one (the fourth column of a token
+  // repeats the third). Columns without a token read one that is there; their sums are not used.
+  int place[CT][4];
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int t = min(F32 ? 4 * ct + (l16 >> 2) : (l16 >> 2) + 4 * (l16 & 3), M - 1);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) place[ct][m] = x_place(F32 ? 3 * t + min(l16 & 3, 2) : t, 4 * m + c);
+  }
+
+  float out[Q];
+  const Unpack<BF> unpack;
+  const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+  const v4u ones = v4u{keep(one), keep(one), keep(one), keep(one)};
+  constexpr float kOffset = BF ? 16.0f : 0.0f;  // what the operand has above v
+
+  auto compute = [&](const Weights& r, const uint8_t* xj) {
     v4f acc[CT], xs[CT];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const v4u wv = unpack<BF>((uint32_t)r.w[m]);
+      const v4u wv = unpack((uint32_t)r.v[m]);
+      const bool first = m % (4 / S) == 0, last = m % (4 / S) == 4 / S - 1;
+      const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        v4u xv;
-        if constexpr (F32)
-          xv = *reinterpret_cast<const v4u*>(cols + (16 * ct + l16) * kPitch + m * 64 + c * 16);
-        else
-          xv = r.x[m];
-        const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
-        const bool first = m == 0 || FOLDS == 4;
-        acc[ct] = mfma<BF>(wv, xv, first ? zero : acc[ct]);
-        xs[ct] = mfma<BF>(ones, xv, first ? zero : xs[ct]);
+        const v4u xv = *reinterpret_cast<const v4u*>(xj + place[ct][m]);
+        acc[ct] = mfma<BF>(xv, wv, first ? zero : acc[ct]);
+        xs[ct] = mfma<BF>(xv, ones, first ? zero : xs[ct]);
       }
-      if (FOLDS == 4 || m == 3) {
-        const int i = FOLDS == 4 ? m : 0;
+      if (last) {
+        const int g = m / (4 / S);
+        const float sc = r.s.template get<SBF>(g);
+        const float z = kOffset + (zeros ? r.z.template get<SBF>(g) : 8.0f);
 #pragma unroll
-        for (int rr = 0; rr < 4; ++rr) {
-          const float sc = scale_of<SBF>(r.s[i], rr);
-          const float z = ZEROS ? scale_of<SBF>(r.z[ZEROS ? i : 0], rr) : 8.0f;
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct)
-            out[ct][rr] =
-                __builtin_fmaf(sc, __builtin_fmaf(-z, xs[ct][rr], acc[ct][rr]), out[ct][rr]);
+        for (int q = 0; q < Q; ++q) {
+          float a, b;
+          if constexpr (F32) {
+            a = (acc[q][2] + acc[q][1]) + acc[q][0];
+            b = (xs[q][2] + xs[q][1]) + xs[q][0];
+          } else {
+            a = acc[0][q];
+            b = xs[0][q];
+          }
+          out[q] = __builtin_fmaf(sc, __builtin_fmaf(-z, b, a), out[q]);
         }
       }
     }
-    if constexpr (F32) {
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
   };
 
-  Rec cur[kBatch], nxt[kBatch];
+  // The wavefronts' sums, [tile of the batch][wave][q][c][row]: lane (c, row) has token c + 4 q.
+  float* red = reinterpret_cast<float*>(smem + nw * (slots * row_bytes));
+  constexpr int kSums = Q * 64;
+  Weights w[kAhead];
+  Tokens xr[F32 ? XA : 1];
+  if constexpr (ALL && !F32) {
+#pragma unroll 1
+    for (int j = 0; j < rounds; ++j) fetch_x(j, j);
+  }
+  if constexpr (F32) {
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) load(cur[u], wave + u * NW);
-  for (int rec = wave; rec < nrec; rec += kBatch * NW) {
-    const bool more = rec + kBatch * NW < nrec;
-    if (more) {
+    for (int u = 0; u < XA; ++u) load_x(xr[u], u);
+  }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) load(nxt[u], rec + (kBatch + u) * NW);
+  for (int u = 0; u < kAhead; ++u) load_w(w[u], (int)blockIdx.x, u);
+  if constexpr (ALL && F32) {
+#pragma unroll 1
+    for (int j = 0; j < rounds; j += XA) {
+#pragma unroll
+      for (int u = 0; u < XA; ++u) {
+        if (j + u >= rounds) break;
+        put_x(xr[u], j + u);
+        load_x(xr[u], j + u + XA);
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) compute(cur[u]);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) cur[u] = nxt[u];
   }
-
-  // The wavefronts' sums, [wave][column][16 rows], added in the order of the wavefronts; a float32
-  // token's three columns after that, the largest last.
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);
+  if constexpr (ALL && !F32) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  for (int tile0 = blockIdx.x; tile0 < ntiles; tile0 += batch * grid) {
+    int n = 0;
+    for (; n < batch; ++n) {
+      const int tile = tile0 + n * grid;
+      if (tile >= ntiles) break;
 #pragma unroll
-  for (int ct = 0; ct < CT; ++ct)
-    *reinterpret_cast<float4*>(red + ((wave * CT + ct) * 16 + l16) * 16 + 4 * c) =
-        make_float4(out[ct][0], out[ct][1], out[ct][2], out[ct][3]);
-  __syncthreads();
-  for (int i = tid; i < 16 * M; i += 64 * NW) {
-    const int t = i >> 4, row = i & 15;
-    const int j = tile * kG4Rows + row;
-    if (j >= N) continue;
-    auto total = [&](int col) {
-      float v = red[col * 16 + row];
+      for (int q = 0; q < Q; ++q) out[q] = 0.0f;
+      for (int j0 = 0; j0 < rounds; j0 += kAhead) {
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += red[(w * CT * 16 + col) * 16 + row];
-      return v;
-    };
-    float v;
-    if constexpr (F32) v = (total(3 * t + 2) + total(3 * t + 1)) + total(3 * t);
-    else v = total(t);
-    if (epi.bias) v += epi.bias[j];
-    v = activate(v, epi.act);
-    const size_t at = (size_t)t * N + j;
-    if (epi.residual) v += load_as_float(epi.residual, at, y_type);
-    store_float(y, at, y_type, v);
+        for (int u = 0; u < kAhead; ++u) {
+          const int j = j0 + u;
+          if (j >= rounds) break;
+          if constexpr (!ALL && F32) {
+            put_x(xr[u % XA], 0);
+            load_x(xr[u % XA], j + XA < rounds ? j + XA : u % XA);
+          }
+          if constexpr (!ALL && !F32) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the last record's operands have been read
+            fetch_x(j, 0);
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+          }
+          compute(w[u], xw + (ALL ? j : 0) * row_bytes);
+          if (j + kAhead < rounds) load_w(w[u], tile, j + kAhead);
+          else load_w(w[u], tile + grid, u);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) red[(n * nw + wave) * kSums + q * 64 + lane] = out[q];
+    }
+    __syncthreads();
+    for (int i = tid; i < n * kSums; i += threads) {
+      const int b = i / kSums, e = i - b * kSums;
+      const int t = ((e >> 4) & 3) + 4 * (e >> 6);
+      const int j = (tile0 + b * grid) * kG4Rows + (e & 15);
+      if (t >= M || j >= N) continue;
+      const float* r = red + b * nw * kSums + e;
+      float v = r[0];
+      for (int k = 1; k < nw; ++k) v += r[k * kSums];
+      if (epi.bias) v += epi.bias[j];
+      v = activate(v, epi.act);
+      const size_t at = (size_t)t * N + j;
+      if (epi.residual) v += load_as_float(epi.residual, at, y_type);
+      store_float(y, at, y_type, v);
+    }
+    if (tile0 + batch * grid < ntiles) __syncthreads();  // the sums have been read
   }
 }
 
-constexpr int64_t lds_bytes(int x_type, int ct, int nw) {
-  const int64_t red = (int64_t)nw * ct * 16 * 16 * 4;
-  const int64_t cols = x_type == kTypeF32 ? (int64_t)nw * 16 * ct * kPitch : 0;
-  return red > cols ? red : cols;
-}
+// Groups of four tokens that a kernel is built for.
+constexpr int token_groups(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : 4; }
 
-// Wavefronts of a workgroup.
-int wavefronts(const Q4GShape&, int64_t) { return 8; }
+// How a call is laid out: wavefronts of a workgroup, records of each that x is in LDS for, tiles whose sums
+// are added together, workgroups, and the LDS.
+struct Plan {
+  int64_t nw, slots, batch, grid, lds;
+  bool all;
+};
+Plan plan(int x_type, int64_t M, const Q4GShape& g, int64_t cus) {
+  constexpr int64_t kLds = 160 << 10;
+  Plan p;
+  const int q = token_groups(M);
+  // 8 wavefronts instead of 16: where less than half of the compute units have a tile, and, two workgroups
+  // to a unit, where every unit has several and a tile's sums are few.
+  const bool several = g.tiles() >= 2 * cus && q == 1 && x_type != kTypeF32;
+  const int64_t per = several ? 2 : 1;
+  p.nw = several || 2 * g.tiles() < cus ? 8 : max_waves(x_type, q);
+  while (p.nw > 1 && p.nw > g.records()) p.nw /= 2;
+  p.grid = std::min(g.tiles(), per * cus);
+  const int64_t row = p.nw * x_rows(x_type, M) * kRowBytes, sums = p.nw * q * 256;
+  p.slots = (g.records() + p.nw - 1) / p.nw;
+  // one tile: float32 values on their way into LDS between the records, not all before the first
+  p.all = p.slots * row + sums <= kLds / per && (x_type != kTypeF32 || g.tiles() > cus);
+  if (!p.all) p.slots = 1;
+  const int64_t most = (g.tiles() + p.grid - 1) / p.grid;
+  p.batch = std::max<int64_t>(1, std::min(most, (kLds / per - p.slots * row) / sums));
+  p.lds = p.slots * row + p.batch * sums;
+  return p;
+}
 
 struct Call {
   const void* x;
@@ -279,110 +420,106 @@ struct Call {
   void* y;
   int y_type;
   int64_t M;
+  Plan p;
   Q4GShape g;
   Q4GEpilogue epi;
 };
 
-template <int XT, int CT, int FOLDS, bool ZEROS, bool SBF, int NW>
-hipError_t launch_t(const Call& c, hipStream_t s) {
-  auto kern = q4g_kernel<XT, CT, FOLDS, ZEROS, SBF, NW>;
-  constexpr int64_t lds = lds_bytes(XT, CT, NW);
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+template <int XT, int Q, int S, bool SBF, bool ALL>
+hipError_t launch_k(const Call& c, hipStream_t s) {
+  auto kern = q4g_kernel<XT, Q, S, SBF, ALL>;
+  if (c.p.lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, (int)c.p.lds);
     if (e != hipSuccess) return e;
   }
-  const int group = (int)(c.g.group < c.g.K ? c.g.group : c.g.K);
-  hipLaunchKernelGGL(kern, dim3((unsigned)c.g.tiles()), dim3(64 * NW), (size_t)lds, s, c.x, c.rep,
-                     c.y, c.y_type, (int)c.M, (int)c.g.N, (int)c.g.K, group,
-                     (size_t)c.g.scales_at(), (size_t)c.g.zeros_at(), c.epi);
+  hipLaunchKernelGGL(kern, dim3((unsigned)c.p.grid), dim3((unsigned)(64 * c.p.nw)), (size_t)c.p.lds, s,
+                     c.x, c.rep, c.y, c.y_type, (int)c.M, (int)c.g.N, (int)c.g.K, (int)c.g.zeros,
+                     (int)c.p.batch, c.epi);
   return hipGetLastError();
 }
 
-template <int XT, int CT, int NW>
-hipError_t launch_type(const Call& c, int scale_type, hipStream_t s) {
-  const bool one = c.g.group % kG4Values == 0 || c.g.group >= c.g.K;
-  const bool sbf = scale_type == kTypeBF16;
-  auto pick = [&](auto z, auto b) {
-    constexpr bool Z = decltype(z)::value, B = decltype(b)::value;
-    return one ? launch_t<XT, CT, 1, Z, B, NW>(c, s) : launch_t<XT, CT, 4, Z, B, NW>(c, s);
-  };
-  constexpr std::integral_constant<bool, true> yes{};
-  constexpr std::integral_constant<bool, false> no{};
-  return c.g.zeros ? (sbf ? pick(yes, yes) : pick(yes, no)) : (sbf ? pick(no, yes) : pick(no, no));
+template <int XT, int Q, int S, bool SBF>
+hipError_t launch_t(const Call& c, hipStream_t s) {
+  return c.p.all ? launch_k<XT, Q, S, SBF, true>(c, s) : launch_k<XT, Q, S, SBF, false>(c, s);
 }
 
-template <int NW>
-hipError_t launch_nw(const Call& c, int x_type, int scale_type, hipStream_t s) {
-  if (x_type == kTypeF16) return launch_type<kTypeF16, 1, NW>(c, scale_type, s);
-  if (x_type == kTypeBF16) return launch_type<kTypeBF16, 1, NW>(c, scale_type, s);
-  switch (column_tiles(kTypeF32, c.M)) {
-    case 1: return launch_type<kTypeF32, 1, NW>(c, scale_type, s);
-    case 2: return launch_type<kTypeF32, 2, NW>(c, scale_type, s);
-    default: return launch_type<kTypeF32, 3, NW>(c, scale_type, s);
+template <int XT, int Q>
+hipError_t launch_q(const Call& c, bool sbf, hipStream_t s) {
+  switch (c.g.scales()) {
+    case 1: return sbf ? launch_t<XT, Q, 1, true>(c, s) : launch_t<XT, Q, 1, false>(c, s);
+    case 2: return sbf ? launch_t<XT, Q, 2, true>(c, s) : launch_t<XT, Q, 2, false>(c, s);
+    default: return sbf ? launch_t<XT, Q, 4, true>(c, s) : launch_t<XT, Q, 4, false>(c, s);
   }
 }
 
-// One work-item per dword of the values, one per scale and per zero.
-__global__ __launch_bounds__(256) void repack_values_kernel(const uint8_t* __restrict__ w,
-                                                            uint32_t* __restrict__ rep, int64_t N,
-                                                            int64_t K, int64_t nrec, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t at = i >> 8;  // (tile, record)
-  const int64_t tile = at / nrec, rec = at - tile * nrec;
-  const int q = (int)(i & 255), m = q & 3, row = (q >> 2) & 15, c = q >> 6;
-  const int64_t j = tile * kG4Rows + row, k = rec * kG4Values + 32 * m + 8 * c;
-  uint32_t o = 0;
-  if (j < N && k < K) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(w + (j * K + k) / 2);
-    // nibble e of v (value e) goes to nibble e / 2 + 4 (e % 2)
+template <int XT>
+hipError_t launch_x(const Call& c, bool sbf, hipStream_t s) {
+  switch (token_groups(c.M)) {
+    case 1: return launch_q<XT, 1>(c, sbf, s);
+    case 2: return launch_q<XT, 2>(c, sbf, s);
+    default: return launch_q<XT, 4>(c, sbf, s);
+  }
+}
+
+// One work-item per dword of the values, and one per scale and zero, of a record.
+__global__ __launch_bounds__(256) void repack_kernel(const uint8_t* __restrict__ w,
+                                                     const uint16_t* __restrict__ scales,
+                                                     const uint16_t* __restrict__ zeros,
+                                                     uint8_t* __restrict__ rep, int64_t N, int64_t K,
+                                                     int64_t group, int64_t nrec, int64_t ngroups,
+                                                     int S, int rec_bytes) {
+  const int64_t tile = (int64_t)blockIdx.x / nrec, rec = (int64_t)blockIdx.x - tile * nrec;
+  uint8_t* out = rep + (int64_t)blockIdx.x * rec_bytes;
+  const int q = threadIdx.x;
+  {
+    const int m = q & 3, row = (q >> 2) & 15, c = q >> 6;
+    const int64_t j = tile * kG4Rows + row, k = rec * kG4Values + 32 * m + 8 * c;
+    uint32_t o = 0;
+    if (j < N && k < K) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(w + (j * K + k) / 2);
+      // nibble e of v (value e) goes to nibble e / 2 + 4 (e % 2)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o |= ((v >> (4 * e)) & 15u) << (4 * (e / 2 + 4 * (e % 2)));
+      for (int e = 0; e < 8; ++e) o |= ((v >> (4 * e)) & 15u) << (4 * (e / 2 + 4 * (e % 2)));
+    }
+    reinterpret_cast<uint32_t*>(out)[q] = o;
   }
-  rep[i] = o;
-}
-__global__ __launch_bounds__(256) void repack_scales_kernel(const uint16_t* __restrict__ s,
-                                                            uint16_t* __restrict__ rep, int64_t N,
-                                                            int64_t ngroups, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  const int64_t at = i >> 4;  // (tile, group)
-  const int64_t tile = at / ngroups, g = at - tile * ngroups;
-  const int64_t j = tile * kG4Rows + (i & 15);
-  rep[i] = j < N ? s[j * ngroups + g] : (uint16_t)0;
+  const int n = kG4Rows * S;
+  if (q < (zeros ? 2 * n : n)) {
+    const uint16_t* src = q < n ? scales : zeros;
+    const int i = q < n ? q : q - n;
+    const int64_t j = tile * kG4Rows + i / S;
+    const int64_t k = rec * kG4Values + (i % S) * (kG4Values / S);
+    reinterpret_cast<uint16_t*>(out + kG4ValueBytes)[q] =
+        j < N && k < K ? src[j * ngroups + k / group] : (uint16_t)0;
+  }
 }
 
 }  // namespace
 
 int64_t q4g_lds_bytes(int x_type, int64_t M, const Q4GShape& g, int64_t compute_units) {
-  return lds_bytes(x_type, column_tiles(x_type, M), wavefronts(g, compute_units));
+  return plan(x_type, M, g, compute_units).lds;
 }
 
 hipError_t launch_q4g(const void* x, int x_type, const void* rep, int scale_type, void* y,
                       int y_type, int64_t M, const Q4GShape& g, const Q4GEpilogue& epi,
                       int64_t compute_units, hipStream_t s) {
-  const Call c{x, static_cast<const uint8_t*>(rep), y, y_type, M, g, epi};
-  (void)compute_units;
-  return launch_nw<8>(c, x_type, scale_type, s);
+  const Call c{x, static_cast<const uint8_t*>(rep), y, y_type, M, plan(x_type, M, g, compute_units), g,
+               epi};
+  const bool sbf = scale_type == kTypeBF16;
+  return x_type == kTypeF32   ? launch_x<kTypeF32>(c, sbf, s)
+         : x_type == kTypeF16 ? launch_x<kTypeF16>(c, sbf, s)
+                              : launch_x<kTypeBF16>(c, sbf, s);
 }
 
 hipError_t launch_repack_q4g(const void* w, const void* scales, const void* zeros,
                              const Q4GShape& g, void* rep, hipStream_t s) {
-  uint8_t* base = static_cast<uint8_t*>(rep);
-  const int64_t n = g.scales_at() / 4, ns = g.tiles() * g.groups() * 16;
-  hipLaunchKernelGGL(repack_values_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                     static_cast<const uint8_t*>(w), reinterpret_cast<uint32_t*>(base), g.N, g.K,
-                     g.records(), n);
-  hipError_t e = hipGetLastError();
-  for (int i = 0; e == hipSuccess && i < (g.zeros ? 2 : 1); ++i) {
-    hipLaunchKernelGGL(repack_scales_kernel, dim3((unsigned)((ns + 255) / 256)), dim3(256), 0, s,
-                       static_cast<const uint16_t*>(i ? zeros : scales),
-                       reinterpret_cast<uint16_t*>(base + (i ? g.zeros_at() : g.scales_at())), g.N,
-                       g.groups(), ns);
-    e = hipGetLastError();
-  }
-  return e;
+  static_assert(2 * kG4Rows * 4 <= 256, "a work-item per scale and zero");
+  hipLaunchKernelGGL(repack_kernel, dim3((unsigned)(g.tiles() * g.records())), dim3(256), 0, s,
+                     static_cast<const uint8_t*>(w), static_cast<const uint16_t*>(scales),
+                     static_cast<const uint16_t*>(zeros), static_cast<uint8_t*>(rep), g.N, g.K,
+                     g.group, g.records(), g.groups(), g.scales(), (int)g.record_bytes());
+  return hipGetLastError();
 }
 
 }  // namespace mmq

@@ -12,14 +12,16 @@ namespace mmq {
 // enum mmq_type, restated for the kernels
 constexpr int kTypeF32 = 0, kTypeF16 = 1, kTypeBF16 = 2;
 
-// Repacked weights: first the values, one 1024-byte record per (tile of 16 rows, 128 values),
-// [tile][record]; then at a 256-byte boundary the scales, 16-bit [tile][group][16 rows]; then, the
-// same way, the zeros. Rows past N and values past K are 0. A record holds dwords
-// [c 0..3][row 0..15][m 0..3] of the 8 values k = 128 record + 32 m + 8 c + e of a row: value e = 2 j
-// in nibble j, e = 2 j + 1 in nibble j + 4, so that one 16-byte load per lane gives the rows of four
-// 16 x 16 x 32 matrix instructions, and an AND and a shift by at most 12 bits the two halves of each
-// operand register.
-constexpr int kG4Rows = 16, kG4Values = 128, kG4RecBytes = 1024;
+// Repacked weights: one record per (tile of 16 rows, 128 values), [tile][record], rows past N and
+// values past K being 0. A record holds
+//   1024 bytes  dwords [c 0..3][row 0..15][m 0..3] of the 8 values k = 128 record + 32 m + 8 c + e of a
+//               row: value e = 2 j in nibble j, e = 2 j + 1 in nibble j + 4. One 16-byte load per lane is
+//               what four 16 x 16 x 32 matrix instructions take, and a shift and an AND make two values
+//               of a dword an operand register.
+//   32 S bytes  16-bit scales [row][S], and, where there are zeros, as many bytes of those. S is how
+//               many scales a row has in a record: 1 where its 128 values lie in one group, 2 for groups
+//               of 64, else 4, one per 32 values.
+constexpr int kG4Rows = 16, kG4Values = 128, kG4ValueBytes = 1024;
 constexpr int kG4MaxTokens = 16;
 
 struct Q4GShape {
@@ -28,11 +30,13 @@ struct Q4GShape {
   constexpr int64_t tiles() const { return (N + kG4Rows - 1) / kG4Rows; }
   constexpr int64_t records() const { return (K + kG4Values - 1) / kG4Values; }
   constexpr int64_t groups() const { return (K + group - 1) / group; }
-  constexpr int64_t scales_at() const { return tiles() * records() * kG4RecBytes; }
-  constexpr int64_t zeros_at() const { return round256(scales_at() + tiles() * groups() * 32); }
-  constexpr int64_t bytes() const {
-    return zeros ? zeros_at() + tiles() * groups() * 32 : scales_at() + tiles() * groups() * 32;
+  constexpr int scales() const {
+    return group % kG4Values == 0 || group >= K ? 1 : group == kG4Values / 2 ? 2 : 4;
   }
+  constexpr int64_t record_bytes() const {
+    return kG4ValueBytes + 2 * kG4Rows * scales() * (zeros ? 2 : 1);
+  }
+  constexpr int64_t bytes() const { return tiles() * records() * record_bytes(); }
 };
 
 struct Q4GEpilogue {

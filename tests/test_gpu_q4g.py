@@ -51,7 +51,9 @@ class Matrix:
         mmq.repack_q4_G(self.w, self.s, self.z, N, K, self.format, self.rep)
 
     def product(self, x):
-        return qo.product(np64(x), self.w.cpu().numpy(), np64(self.s), np64(self.z), self.group)
+        # bf16 operands (those of float32 tokens too) hold 16 + v
+        return qo.product(np64(x), self.w.cpu().numpy(), np64(self.s), np64(self.z), self.group,
+                          0.0 if x.dtype == torch.float16 else 16.0)
 
 
 def tokens(M, K, t, seed):
@@ -179,30 +181,32 @@ def test_wide_and_long():
         check(Matrix(N, K, group, seed=1), tokens(M, K, x, 2))
 
 
-def test_repack_layout():
-    """The records as documented: dwords [c][row][m], nibbles j and j + 4 of two neighbouring values."""
-    N, K, group = 35, 288, 96
-    m = Matrix(N, K, group, seed=11)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group,S", [(96, 4), (64, 2), (128, 1), (288, 1)])
+def test_repack_layout(group, S, zeros):
+    """The records as documented: dwords [c][row][m], nibbles j and j + 4 of two neighbouring values, then
+    S scales and S zeros of every row."""
+    N, K = 35, 288
+    m = Matrix(N, K, group, zeros=zeros, seed=11)
     torch.cuda.synchronize()
-    img = m.rep.cpu().numpy()
     v = np.zeros((48, 384), np.int64)
     v[:N, :K] = qo.values(m.w.cpu().numpy())
     want = np.zeros((3, 3, 4, 16, 4), np.uint32)
     for e in range(8):
         part = v.reshape(3, 16, 3, 4, 4, 8)[..., e]           # tile, row, record, m, c
         want |= (part.transpose(0, 2, 4, 1, 3) << (4 * (e // 2 + 4 * (e % 2)))).astype(np.uint32)
-    n = want.size * 4
-    assert np.array_equal(img[:n].view(np.uint32), want.reshape(-1))
-    s = np.zeros((48, 3), np.uint16)
-    s[:N] = m.s.cpu().view(torch.int16).numpy().view(np.uint16)
-    assert np.array_equal(img[n:n + 2 * s.size].view(np.uint16),
-                          s.reshape(3, 16, 3).transpose(0, 2, 1).reshape(-1))
-    z = np.zeros((48, 3), np.uint16)
-    z[:N] = m.z.cpu().view(torch.int16).numpy().view(np.uint16)
-    at = (n + 2 * s.size + 255) // 256 * 256
-    assert np.array_equal(img[at:at + 2 * z.size].view(np.uint16),
-                          z.reshape(3, 16, 3).transpose(0, 2, 1).reshape(-1))
-    assert img.size == at + 2 * z.size
+    img = m.rep.cpu().numpy().reshape(3, 3, -1)
+    assert np.array_equal(img[..., :1024].copy().view(np.uint32), want.reshape(3, 3, -1))
+    at = 1024
+    for t in (m.s, m.z)[:1 + zeros]:
+        bits = t.cpu().view(torch.int16).numpy().view(np.uint16)
+        s = np.zeros((48, 3 * S), np.uint16)
+        k = np.arange(3 * S) * (128 // S)
+        s[:N, k < K] = bits[:, k[k < K] // group]
+        got = img[..., at:at + 32 * S].copy().view(np.uint16).reshape(3, 3, 16, S)
+        assert np.array_equal(got, s.reshape(3, 16, 3, S).transpose(0, 2, 1, 3))
+        at += 32 * S
+    assert img.shape[2] == at
 
 
 def test_decode_step_in_a_graph_and_on_two_streams():

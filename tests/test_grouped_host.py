@@ -133,10 +133,13 @@ def q4g(M=1, N=64, K=256, xt=1, x=P, w=P, f=None, yt=1, y=P, epi=None):
 
 
 def test_q4g_bytes():
-    # 3 tiles of 16 rows, 3 records of 128 values and groups of 96: ceil(288 / 96) = 3
-    assert mmq.mmq_q4G_repacked_bytes(35, 288, fmt(96, zeros=0)) == 9 * 1024 + 9 * 32
-    assert mmq.mmq_q4G_repacked_bytes(35, 288, fmt(96)) == 9 * 1024 + 2 * 256 + 9 * 32
-    assert mmq.mmq_q4G_repacked_bytes(16, 100 * 32, fmt(1 << 20, zeros=0)) == 25 * 1024 + 32
+    # 3 tiles of 16 rows by 3 records of 128 values, each with 1024 bytes of values and, per row, one
+    # 16-bit scale per 32 values, per 64 or per record, and as many zeros
+    for group, scales in ((32, 4), (64, 2), (96, 4), (128, 1), (160, 4), (256, 1), (288, 1),
+                          (1 << 20, 1)):
+        for zeros in (0, 1):
+            assert mmq.mmq_q4G_repacked_bytes(35, 288, fmt(group, zeros=zeros)) == (
+                9 * (1024 + 32 * scales * (1 + zeros)))
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -216,10 +219,11 @@ def test_calls_check_buffers_against_the_size_of_the_call(fn, args, monkeypatch)
 
 
 @pytest.mark.skipif(not m0.os.path.exists(m0.build.HIPCC), reason="hipcc not found")
-def test_compiler_leaves_m0_to_the_loads_in_the_grouped_products():
+@pytest.mark.parametrize("source", ["grouped.hip", "q4g.hip"])
+def test_compiler_leaves_m0_to_the_loads_into_lds(source):
     tmp = tempfile.mkdtemp(prefix="m0_check_")
     try:
-        path = m0.assembly("grouped.hip", tmp)
+        path = m0.assembly(source, tmp)
         assert "buffer_load_dwordx4" in open(path).read()
         assert not m0.compiler_m0_uses(path)
     finally:
