@@ -99,11 +99,11 @@ __device__ __forceinline__ int scan_experts(SortLds& sh, int n, int E) {
 }
 
 template <int NI>
-__device__ __forceinline__ void write_places(const SortLds& sh, int64_t p0, int64_t P, int E,
+__device__ __forceinline__ void write_places(const SortLds& sh, int64_t P, int E,
                                              int all, const int (&id)[NI], const int (&rank)[NI],
                                              int* __restrict__ order, int* __restrict__ place) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = p0 + (int64_t)wave * (64 * NI) + lane;
+  const int64_t first = (int64_t)wave * (64 * NI) + lane;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int64_t p = first + 64 * i;
@@ -129,41 +129,74 @@ __global__ __launch_bounds__(kThreads) void group_kernel(const int* __restrict__
   const GroupLayout g{P, E};
   if ((int)threadIdx.x < E) groups[threadIdx.x] = sh.base[threadIdx.x];
   if (threadIdx.x == 0) groups[E] = all;
-  write_places<NI>(sh, 0, P, E, all, id, rank, groups + g.order(), groups + g.place());
+  write_places<NI>(sh, P, E, all, id, rank, groups + g.order(), groups + g.place());
 }
 
-// Many pairs, in chunks of kGroupChunk: the counts of each chunk ...
+// Many pairs, in chunks of kGroupChunk: the counts of each chunk, and in `place` the rank of each pair in
+// its chunk ...
 constexpr int kChunkNI = kGroupChunk / kThreads;
 __global__ __launch_bounds__(kThreads) void count_kernel(const int* __restrict__ ids, int64_t P,
                                                          int E, int bits, int* __restrict__ groups) {
   __shared__ SortLds sh;
-  int id[kChunkNI], rank[kChunkNI], total;
-  rank_pairs<kChunkNI>(sh, ids, (int64_t)blockIdx.x * kGroupChunk, P, E, bits, id, rank, total);
-  if ((int)threadIdx.x < E)
-    groups[GroupLayout{P, E}.counts() + (int64_t)blockIdx.x * E + threadIdx.x] = total;
-}
-
-// ... and, with those of the chunks before it, the places of a chunk's pairs (ranked again: that
-// takes less than a trip of the ranks through memory).
-__global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int64_t P,
-                                                         int E, int bits, int* __restrict__ groups) {
-  __shared__ SortLds sh;
-  const int64_t p0 = (int64_t)blockIdx.x * kGroupChunk;
   const GroupLayout g{P, E};
-  const int tid = threadIdx.x;
-  int n = 0, before = 0;
-  if (tid < E) {
-    const int* c = groups + g.counts() + tid;
-    const int chunks = (int)g.chunks();
-#pragma unroll 8
-    for (int i = 0; i < chunks; ++i) {
-      const int v = c[(int64_t)i * E];
-      if (i < (int)blockIdx.x) before += v;
-      n += v;
-    }
-  }
+  const int64_t p0 = (int64_t)blockIdx.x * kGroupChunk;
   int id[kChunkNI], rank[kChunkNI], total;
   rank_pairs<kChunkNI>(sh, ids, p0, P, E, bits, id, rank, total);
+  if ((int)threadIdx.x < E)
+    groups[g.counts() + (int64_t)blockIdx.x * E + threadIdx.x] = total;
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int i = 0; i < kChunkNI; ++i) {
+    const int64_t p = p0 + (int64_t)wave * (64 * kChunkNI) + 64 * i + lane;
+    if (p < P && id[i] < E) groups[g.place() + p] = sh.count[wave][id[i]] + rank[i];
+  }
+}
+
+// ... and, with the counts of the chunks before it, the places. The counts are read by all work-items, one
+// to an expert and a share of the chunks.
+__global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__ ids, int64_t P,
+                                                         int E, int* __restrict__ groups) {
+  __shared__ SortLds sh;
+  const GroupLayout g{P, E};
+  const int64_t p0 = (int64_t)blockIdx.x * kGroupChunk;
+  const int tid = threadIdx.x;
+  int* order = groups + g.order();
+  int* place = groups + g.place();
+  int id[kChunkNI], rank[kChunkNI];
+#pragma unroll
+  for (int i = 0; i < kChunkNI; ++i) {
+    const int64_t p = p0 + i * kThreads + tid;
+    const int v = p < P ? ids[p] : -1;
+    id[i] = v >= 0 && v < E ? v : E;
+    rank[i] = id[i] < E ? place[p] : 0;
+  }
+  int wide = 64;  // experts, rounded up to a power of two
+  while (wide < E) wide *= 2;
+  const int e = tid & (wide - 1), share = tid / wide, shares = kThreads / wide;
+  int n = 0, before = 0;
+  if (e < E) {
+    const int* c = groups + g.counts() + e;
+    const int chunks = (int)g.chunks();
+#pragma unroll 8
+    for (int i = share; i < chunks; i += shares) {
+      const int v = c[(int64_t)i * E];
+      n += v;
+      if (i < (int)blockIdx.x) before += v;
+    }
+  }
+  // shares of an expert in sh.count, as [share][n, before][expert]
+  int* part = &sh.count[0][0];
+  static_assert(2 * kThreads <= kWaves * kGroupMaxExperts, "LDS of the shares");
+  part[2 * share * wide + e] = n;
+  part[(2 * share + 1) * wide + e] = before;
+  __syncthreads();
+  n = before = 0;
+  if (tid < E)
+    for (int i = 0; i < shares; ++i) {
+      n += part[2 * i * wide + tid];
+      before += part[(2 * i + 1) * wide + tid];
+    }
   const int all = scan_experts(sh, n, E);
   if (blockIdx.x == 0) {
     if (tid < E) groups[tid] = sh.base[tid];
@@ -171,7 +204,18 @@ __global__ __launch_bounds__(kThreads) void place_kernel(const int* __restrict__
   }
   if (tid < E) sh.base[tid] += before;
   __syncthreads();
-  write_places<kChunkNI>(sh, p0, P, E, all, id, rank, groups + g.order(), groups + g.place());
+#pragma unroll
+  for (int i = 0; i < kChunkNI; ++i) {
+    const int64_t p = p0 + i * kThreads + tid;
+    if (p >= P) continue;
+    int at = -1;
+    if (id[i] < E) {
+      at = sh.base[id[i]] + rank[i];
+      order[at] = (int)p;
+    }
+    place[p] = at;
+    if (p >= all) order[p] = -1;
+  }
 }
 
 // One work-item per four (or one) columns of a token.
@@ -223,14 +267,14 @@ hipError_t launch_group(const int* ids, int64_t P, int64_t E, int* groups, hipSt
     hipLaunchKernelGGL(group_kernel<1>, dim3(1), dim3(kThreads), 0, s, ids, p, e, bits, groups);
   } else if (P <= 2 * kThreads) {
     hipLaunchKernelGGL(group_kernel<2>, dim3(1), dim3(kThreads), 0, s, ids, p, e, bits, groups);
-  } else if (P <= kGroupChunk) {
+  } else if (P <= kGroupOne) {
     hipLaunchKernelGGL(group_kernel<4>, dim3(1), dim3(kThreads), 0, s, ids, p, e, bits, groups);
   } else {
     const dim3 grid((unsigned)GroupLayout{P, E}.chunks());
     hipLaunchKernelGGL(count_kernel, grid, dim3(kThreads), 0, s, ids, P, e, bits, groups);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL(place_kernel, grid, dim3(kThreads), 0, s, ids, P, e, bits, groups);
+    hipLaunchKernelGGL(place_kernel, grid, dim3(kThreads), 0, s, ids, P, e, groups);
   }
   return hipGetLastError();
 }

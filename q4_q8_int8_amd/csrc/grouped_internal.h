@@ -13,7 +13,8 @@ constexpr int kGroupMaxExperts = 512;
 
 // The groups of P = M*k pairs over E experts, int32, each part at a multiple of four words:
 // offsets[E + 1], order[P], place[P], then the sort's own counts (chunks of pairs by experts).
-constexpr int kGroupChunk = 4096;  // pairs of one workgroup of the sort
+// The sort: pairs of one workgroup that does it alone, and of one of several.
+constexpr int kGroupOne = 4096, kGroupChunk = 2048;
 __host__ __device__ constexpr int64_t round4(int64_t v) { return (v + 3) / 4 * 4; }
 struct GroupLayout {
   int64_t P, E;
@@ -24,7 +25,7 @@ struct GroupLayout {
     return (P + kGroupChunk - 1) / kGroupChunk;
   }
   __host__ __device__ constexpr int64_t words() const {
-    return counts() + (chunks() > 1 ? round4(chunks() * E) : 0);
+    return counts() + (P > kGroupOne ? round4(chunks() * E) : 0);
   }
 };
 

@@ -20,9 +20,9 @@ BIG = 1 << 40
 
 
 def test_group_bytes():
-    # offsets 9 -> 12 words, order and place 6 -> 8 each; then, above 4096 pairs, chunks x experts
+    # offsets 9 -> 12 words, order and place 6 -> 8 each; then, above 4096 pairs, chunks of 2048 x experts
     assert mmq.mmq_moe_group_bytes(3, 8, 2) == 4 * (12 + 8 + 8)
-    assert mmq.mmq_moe_group_bytes(4097, 8, 1) == 4 * (12 + 2 * 4100 + 16)
+    assert mmq.mmq_moe_group_bytes(4097, 8, 1) == 4 * (12 + 2 * 4100 + 24)
     g = torch.zeros(12 + 8 + 8, dtype=torch.int32)
     g[:] = torch.arange(28)
     offsets, order, place = mmq.moe_groups(g, 3, 8, 2)
