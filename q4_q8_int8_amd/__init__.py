@@ -631,10 +631,12 @@ def moe_groups(groups, M: int, E: int, k: int):
     need = _group_sizes(M, E, k)[1]
     if groups.dtype != torch.int32 or not groups.is_contiguous() or groups.nbytes < need:
         raise MMQArgumentError(f"groups: must be a contiguous int32 tensor of {need} bytes or more")
-    P, flat = M * k, groups.flatten()
+    P, at = M * k, groups.storage_offset()
     a = (E + 1 + 3) // 4 * 4
     b = a + (P + 3) // 4 * 4
-    return flat[:E + 1], flat[a:a + P], flat[b:b + P]
+    one = (1,)
+    return (groups.as_strided((E + 1,), one, at), groups.as_strided((P,), one, at + a),
+            groups.as_strided((P,), one, at + b))
 
 
 @_sizes
