@@ -218,10 +218,13 @@ int mmq_moe_group(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* 
  * per_pair = 1: x [M*k][K], a row per pair, r = p. w_rep: E repacked q4_K matrices (N, K) one behind
  * the other; q8: scratch of mmq_q8_1_bytes(rows of x, K) bytes (in a layout of its own).
  * mmq_q4K_grouped_gated: H[p][F] = act(x[p / k] Wg(e)^T) * (x[p / k] Wu(e)^T), x float32 [M][D],
- * w_pairs: E repacked pairs (F, D); q8: scratch of mmq_q8_1_bytes(M, D) bytes. For at most 64 tokens
- * mmq_q4K_moe_gated computes the same with a plan; it is the faster one there.
+ * w_pairs: E repacked pairs (F, D); q8: scratch of mmq_q8_1_bytes(M, D) bytes.
+ * mmq_q4K_moe_gated and _down take up to 64 tokens with a plan; they are the faster ones for few tokens
+ * (gated and down of 8 tokens, 8 of 64 experts, D = 2048, F = 1024: 28 and 16 us against 30 and 24; 2 of
+ * 8, 4096, 11008: 85 and 43 against 100 and 49), and where an expert gets some 4 to 8 of the pairs on
+ * average the two meet (64 tokens: 45 and 37 against 39 and 29; 128 and 76 against 109 and 54).
  * K % 256 == 0, K <= 2^24, (rows of x)*K < 2^31, N <= 2^30, and (M*k/32 + min(E, M*k)) * ceil(N/256)
- * < 2^23 (gated: of its 32 * ceil(F/16) packed rows).
+ * < 2^23 - 8 (gated: of its 32 * ceil(F/16) packed rows).
  * Errors: MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP.
  */
 int mmq_q4K_grouped(int64_t M, int64_t E, int64_t k, int64_t N, int64_t K, const float* x,

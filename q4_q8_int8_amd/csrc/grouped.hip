@@ -627,7 +627,10 @@ GroupedForm grouped_form(const GroupedShape& g, int64_t compute_units) {
       rounds(narrow, 4.0 * cus) * (nsb * us(load) + 5.0),
       rounds(narrow, 2.0 * cus) * (std::ceil(nsb / 2.0) * us(2.0 * load) + 6.0),
       rounds(narrow, cus) * (std::ceil(nsb / 4.0) * 3.5 + 7.0)};
-  return (GroupedForm)(std::min_element(cost, cost + 4) - cost);
+  // Dividing K gains nothing where the narrow tiles fill the device many times over; the bound keeps the
+  // split forms' grids (at most 2.6 times `narrow`, workgroups of up to 1024) far below 2^32 work-items.
+  const int forms = narrow <= 64.0 * cus ? 4 : 2;
+  return (GroupedForm)(std::min_element(cost, cost + forms) - cost);
 }
 
 int64_t grouped_lds_bytes(GroupedForm f) {

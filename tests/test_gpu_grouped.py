@@ -383,6 +383,79 @@ def test_grouped_layer_in_a_graph_and_on_two_streams():
             assert np.array_equal(host(d["out"]), host(eager)), i
 
 
+def test_sort_of_many_pairs_in_a_graph():
+    """The sort in chunks, captured and replayed with other ids in between."""
+    M, E, k = 3001, 60, 2
+    ids = torch.empty(M, k, dtype=torch.int32, device="cuda")
+    g = torch.empty(mmq.mmq_moe_group_bytes(M, E, k) // 4, dtype=torch.int32, device="cuda")
+    ids.fill_(-1)
+    say("sort in a graph")
+    mmq.mmq_moe_group(M, E, k, ids, g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mmq.mmq_moe_group(M, E, k, ids, g)
+    for i, kind in enumerate(("random", "outside", "one", "random")):
+        h = ids_of(kind, M, E, k, i)
+        ids.copy_(torch.from_numpy(h))
+        graph.replay()
+        for got, want in zip(mmq.moe_groups(g, M, E, k), lo.groups(h, E)):
+            assert np.array_equal(host(got), want), i
+
+
+def test_expert_weights_past_4_gib():
+    """The last of 512 experts starts 4.3 GB into the weights; 3 and 200 rows of it."""
+    E, D, F = 512, 4096, 1840
+    n = mmq.mmq_q4K_pair_bytes(F, D)
+    assert (E - 1) * n > 2 ** 32
+    w_in = torch.empty(E * n, dtype=torch.uint8, device="cuda")   # only two experts are written
+    gate = {e: lu.weights(F, D, 2 * e) for e in (0, E - 1)}
+    up = {e: lu.weights(F, D, 2 * e + 1) for e in (0, E - 1)}
+    for e in gate:
+        mmq.repack_q4_K_pair(to_dev(gate[e]), to_dev(up[e]), F, D, w_in[e * n:(e + 1) * n])
+    for M in (3, 200):
+        x = synth.activations("normal", M, D, 3)
+        ids = np.full((M, 1), E - 1, np.int32)
+        ids[1] = 0
+        H = f32(M, F)
+        say("experts past 4 GiB", M)
+        mmq.mmq_q4K_grouped_gated(M, E, 1, F, D, to_dev(x), group(ids, E), w_in, H,
+                                  raw(mmq.mmq_q8_1_bytes(M, D)))
+        got = host(H)
+        for t in (0, 1, 2, M - 1):
+            e = ids[t, 0]
+            (G, TG), (U, TU) = lu.product(x[t:t + 1], gate[e]), lu.product(x[t:t + 1], up[e])
+            lu.assert_close(got[t:t + 1], *lo.gated(G, TG, U, TU, lu.BAR, "silu"))
+
+
+def test_output_past_4_gib():
+    """The last pairs' rows start more than 4 GiB into the output, and into the workspace of the
+    weighted sum."""
+    M, E, k, N, K = 35000, 2, 2, 16400, 256
+    assert (M * k - 8) * N * 4 > 2 ** 32
+    rep, ws, _ = experts("plain", E, N, K, 40)
+    xh = synth.activations("normal", M * k, K, 2)
+    ids = np.random.default_rng(1).integers(0, E, (M, k)).astype(np.int32)
+    g, x = group(ids, E), to_dev(xh)
+    C = f32(M * k, N)
+    say("grouped output past 4 GiB")
+    mmq.mmq_q4K_grouped(M, E, k, N, K, x, g, rep, C, raw(mmq.mmq_q8_1_bytes(M * k, K)),
+                        per_pair=True)
+    wts = np.random.default_rng(2).random((M, k)).astype(np.float32)
+    out = f32(M, N)
+    mmq.mmq_q4K_grouped_down(M, E, k, N, K, x, g, to_dev(wts), rep, out,
+                             raw(mmq.mmq_grouped_down_workspace_bytes(M, E, k, N, K)))
+    for t in (0, 1, M - 3, M - 2, M - 1):
+        ps = np.arange(t * k, t * k + k)
+        for p in ps:
+            P, T = lu.product(np.ascontiguousarray(xh[p:p + 1]), ws[ids.reshape(-1)[p]])
+            lu.assert_close(host(C[p:p + 1]), P, lu.BAR * T)
+        lu.assert_close(host(out[t:t + 1]),
+                        *lu.experts_down(np.ascontiguousarray(xh[ps]), ids[t:t + 1], wts[t:t + 1],
+                                         ws, None))
+    assert bool(torch.isfinite(C).all())
+
+
 def test_groups_of_nonsense_select_rows_of_the_product_only():
     """Every int32 in the groups: the calls return, and write nothing outside their outputs."""
     M, E, k, N, K = 200, 8, 2, 64, 256

@@ -181,6 +181,38 @@ def test_wide_and_long():
         check(Matrix(N, K, group, seed=1), tokens(M, K, x, 2))
 
 
+# tokens that do not fit the LDS for all records of a wavefront: one tile to a workgroup, and several;
+# float32 tokens kept for several tiles; more tiles than one workgroup's sums of them fit the LDS
+@pytest.mark.parametrize("M,N,K,group,x", [
+    (16, 40, 8192, 128, "f16"), (13, 40, 8192, 64, "bf16"), (16, 4200, 8192, 128, "bf16"),
+    (9, 4200, 4096, 32, "f32"), (3, 4200, 512, 64, "f32"), (9, 4200, 256, 128, "f32"),
+    (4, 8300, 640, 64, "f32"), (4, 8300, 1152, 32, "bf16"), (16, 25000, 2048, 256, "bf16"),
+    (16, 32810, 1024, 64, "f32")])
+def test_many_tiles_and_many_tokens(M, N, K, group, x):
+    say("q4_G", (M, N, K), "group", group, x)
+    check(Matrix(N, K, group, seed=4), tokens(M, K, x, 6))
+
+
+def test_weights_past_4_gib():
+    """The last rows' packed values and records start more than 4 GiB into both."""
+    N, K, group = (1 << 21) + 40, 4128, 128
+    n = -(-K // group)
+    f = mmq.q4G_format(group, torch.float16, False)
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    s = torch.rand(N, n, device="cuda").half()
+    rep = torch.empty(mmq.mmq_q4G_repacked_bytes(N, K, f), dtype=torch.uint8, device="cuda")
+    assert (N - 64) * K // 2 > 2 ** 32
+    say("q4_G past 4 GiB")
+    mmq.repack_q4_G(w, s, None, N, K, f, rep)
+    x, y = tokens(2, K, "bf16", 3), torch.full((2, N), NAN, device="cuda")
+    mmq.mmq_q4G(2, N, K, x, rep, f, y)
+    for rows in (slice(0, 20), slice(N - 50, N)):
+        P, T = qo.product(np64(x), w[rows].cpu().numpy(), np64(s[rows]), None, group, 16.0)
+        err = qo.bound(T, K)
+        lu.assert_close(np64(y[:, rows]), P, rounded(P, err, "f32"))
+    assert bool(torch.isfinite(y).all())
+
+
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("group,S", [(96, 4), (64, 2), (128, 1), (288, 1)])
 def test_repack_layout(group, S, zeros):

@@ -9,6 +9,7 @@ import pytest
 
 from oracle import layer_oracle as lo
 from oracle import q4g_oracle as qo
+from tests import grouped_util as gu
 from tests import test_m0_reservation as m0
 
 mmq = pytest.importorskip("q4_q8_int8_amd")
@@ -92,6 +93,23 @@ def test_grids_stay_below_2_to_the_32_work_items():
     a = list(CALLS["down"](1 << 20, 8, 1))
     a[4] = 16 * 256                               # 2^24 workgroups of the weighted sum
     assert mmq.raw_call(*a) == mmq.MMQ_E_SHAPE
+
+
+def test_every_forms_grid_stays_below_2_to_the_32_work_items():
+    """At the largest products that the calls take, whatever form is chosen; workgroups come in eights."""
+    tile = {"wide": (128, 256, 512), "narrow": (32, 128, 256), "split2": (32, 128, 512),
+            "split4": (32, 128, 1024)}
+    for P in (1, 40, 512, 5000, 100000, 1 << 21):
+        for E in (1, 7, 64, 512):
+            most = P // 32 + min(E, P)
+            for K in (256, 4096, 1 << 18, 1 << 24):
+                for share in (1, 2, 16, 300, 3000):
+                    N = min(((1 << 23) - 9) // share // most * 256, 1 << 30)
+                    if N == 0:
+                        continue
+                    rows, cols, threads = tile[gu.grouped_form(P, E, N, K)]
+                    grid = (P // rows + min(E, P)) * -(-N // cols)
+                    assert (grid + 7) // 8 * 8 * threads < 2 ** 32, (P, E, N, K)
 
 
 @pytest.mark.parametrize("call,i,v", [
