@@ -32,6 +32,8 @@
 namespace mmq {
 namespace {
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+
 __device__ __forceinline__ void set_priority(int p) {
   if (p >= 3) __builtin_amdgcn_s_setprio(3);
   else if (p == 2) __builtin_amdgcn_s_setprio(2);
@@ -164,7 +166,7 @@ struct Loads {
   __amdgpu_buffer_rsrc_t rw;
   uint32_t a_off[F::kAOps], da_off[F::kDaOps], tp_off[F::kPOps];
   uint32_t tp_step;
-  int parts, cw, wave, lane;
+  int parts, slots, cw, wave, lane;
   bool works;  // whether the wavefront has a weight tile
   uint32_t lds0, tok_at, hdr_at;
 
@@ -191,6 +193,7 @@ struct Loads {
     rwd = make_rsrc_sgpr(wtile, (uint32_t)tile_bytes);
     rw = make_rsrc(wtile, (uint32_t)tile_bytes);
     parts = (t.rows + 31) >> 5;
+    slots = (t.rows <= 16 ? 16 : parts * 32) * 17;
   }
   // Its tokens: a row past the last, and the padding, read past the buffers' ends (zero), and stay there
   // with every super-block.
@@ -216,7 +219,7 @@ struct Loads {
       tp_off[j] = src < M ? ((uint32_t)(q / F::BM) * M + src) * 16u : M * (K >> 8) * 48u;
     }
   }
-  // Instruction v of super-block s into stage p; those of parts that the tile does not have are left out.
+  // Instruction v of super-block s into stage p; those of rows that the tile does not have are left out.
   __device__ __forceinline__ void issue(int v, int s, int p) const {
     const uint32_t st = lds0 + (uint32_t)p * F::kStage + tok_at;
     if (v < 1) {
@@ -228,7 +231,7 @@ struct Loads {
     v -= 1;
     if (v < F::kAOps) {
       const int k = cw + v * F::CW;
-      if (k * 64 < parts * (32 * 17)) dma(rq, st, k, F::BM * 17, a_off[v] + (uint32_t)s * 256);
+      if (k * 64 < slots) dma(rq, st, k, F::BM * 17, a_off[v] + (uint32_t)s * 256);
       return;
     }
     v -= F::kAOps;
@@ -248,6 +251,17 @@ struct Loads {
   }
   __device__ __forceinline__ v4i nibbles(int s, int gi) const {
     return buf_load16(rw, (uint32_t)s * kRepTileBytes + gi * 1024 + lane * 16);
+  }
+  // The same two blocks for the tile of 16 rows: the lane (r, c) has values 8 c .. 8 c + 7 of both of weight
+  // row r in x, y, and of row 16 + r in z, w.
+  __device__ __forceinline__ v4i nibbles16(int s, int gi) const {
+    const int at = gi * 1024 + (lane >> 5) * 512 + (lane & 15) * 16 + ((lane >> 4) & 1) * 8;
+    const int so = s * kRepTileBytes;
+    const uint2 a =
+        __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rw, at, so, 0));
+    const uint2 b =
+        __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rw, at + 256, so, 0));
+    return v4i{(int)a.x, (int)a.y, (int)b.x, (int)b.y};
   }
 };
 
@@ -399,6 +413,132 @@ __device__ __forceinline__ void sums(uint8_t* smem, const Loads<F>& ld, int s0, 
   }
 }
 
+// The same for a tile of at most 16 rows: the 32 weight rows are two tiles of 16 x 16, half the elements to
+// rescale. Lane (r, c) has token r and, in acc[w], weight rows 16 w + 4 c .. + 3. raw as nibbles16.
+template <class F>
+__device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0, int s1, int steps,
+                                       v4i (&raw)[4], v4f (&acc)[2]) {
+  const int lane = ld.lane, r16 = lane & 15, c = lane >> 4;
+  v4i bias;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) bias[r] = kBiasBits;
+  asm volatile("" : "+v"(bias));
+  acc[0] = acc[1] = v4f{0.f, 0.f, 0.f, 0.f};
+  // term2's piece pairs (weights, tokens): (0, 0) (0, 1) (1, 0) (0, 2), then (1, 1) (2, 0)
+  const int ia = c == 2 ? 1 : 0, jb = c == 1 ? 1 : (c == 3 ? 2 : 0);
+  const int ib = c == 0 ? 1 : 2, jc = c == 0 ? 1 : 0;
+  for (int i = 0; i < steps; ++i) {
+    const int s = s0 + i, p = i & 1;
+    const bool more = s + 1 < s1;
+    v4i next[4];
+    if ((F::KS == 1 || s < s1) && ld.works) {
+      const uint8_t* st = smem + p * F::kStage + ld.tok_at;
+      const uint8_t* sArow = st + r16 * kRowStride + c * 8;
+      const uint8_t* sDa = st + F::kTokA + r16 * 16;
+      const uint8_t* sTp = st + F::kTokA + F::kTokDa;
+      uint8_t* sW = smem + 2 * F::kStage + ld.wave * F::kExpanded;
+      const float* sWw = reinterpret_cast<const float*>(sW);
+      const v4i hdr =
+          *reinterpret_cast<const v4i*>(smem + p * F::kStage + ld.hdr_at + (lane & 31) * 16);
+      q4k_stage_scales(hdr, lane & 31, lane >= 32, sW);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        if (b % 2 == 0) set_priority(3 - b / 2);
+        if (more) {
+          if (b == 0) {
+#pragma unroll
+            for (int gi = 0; gi < 4; ++gi) next[gi] = ld.nibbles16(s + 1, gi);
+          }
+#pragma unroll
+          for (int v = 0; v < F::kOps; ++v)
+            if ((v / 3 * 2 < 7 ? v / 3 * 2 : 7) == b) ld.issue(v, s + 1, p ^ 1);
+        }
+        uint2 tok = *reinterpret_cast<const uint2*>(sArow + b * 32);
+        asm volatile("" : "+v"(tok.x), "+v"(tok.y));  // the steps stay in order
+        const float2 da = *reinterpret_cast<const float2*>(sDa + (b >> 1) * F::BM * 16 + (b & 1) * 8);
+        const long top = __builtin_bit_cast(long, tok);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t x = (uint32_t)raw[b >> 1][2 * w], y = (uint32_t)raw[b >> 1][2 * w + 1];
+          const uint2 wv = b & 1 ? make_uint2((x >> 4) & 0x0F0F0F0Fu, (y >> 4) & 0x0F0F0F0Fu)
+                                 : make_uint2(x & 0x0F0F0F0Fu, y & 0x0F0F0F0Fu);
+          const v4i D = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(long, wv), top, bias,
+                                                              0, 0, 0);
+          const float4 d = *reinterpret_cast<const float4*>(sWw + b * 32 + 16 * w + 4 * c);
+          const float ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int Dr = D[r];
+            acc[w][r] = __builtin_fmaf(__builtin_fmaf(__int_as_float(Dr), da.x, da.y), ds[r], acc[w][r]);
+          }
+        }
+        if (b == 1 || b == 3) {
+          const bool zero = b == 3 && c >= 2;
+          const int wi = b == 1 ? ia : ib, ti = b == 1 ? jb : jc;
+          v4i tb = *reinterpret_cast<const v4i*>(sTp + (ti * F::BM + r16) * 16);
+          if (zero) tb = v4i{0, 0, 0, 0};
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            v4i wa =
+                *reinterpret_cast<const v4i*>(sW + kWDsvBytes + (wi * 32 + 16 * w + r16) * 16);
+            if (zero) wa = v4i{0, 0, 0, 0};
+            acc[w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(v8bf, wa), __builtin_bit_cast(v8bf, tb), acc[w], 0, 0, 0);
+          }
+        }
+      }
+    } else if (more) {
+#pragma unroll
+      for (int v = 0; v < F::kOps; ++v) ld.issue(v, s + 1, p ^ 1);
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int gi = 0; gi < 4; ++gi) raw[gi] = next[gi];
+  }
+}
+
+// Out of the lanes' registers: four of a row to 64 bytes (gated: two, the lanes of the gate and the up values
+// of one output changing one half of them).
+template <int EPI>
+__device__ __forceinline__ void store16(const int2* rows, const Args& g, int wt, int lane,
+                                        const v4f (&acc)[2], const EpiParam<EPI>& epi) {
+  const int c = lane >> 4, pair = rows[lane & 15].x;
+  const bool ok = pair >= 0 && wt < (g.N + 31) >> 5;
+  auto put = [&](int cols, int j, float a, float b, float d, float e) {
+    float* o = g.out + (size_t)pair * cols + j;
+    if ((cols & 3) == 0 && j + 3 < cols) {
+      *reinterpret_cast<float4*>(o) = make_float4(a, b, d, e);
+    } else {
+      if (j + 0 < cols) o[0] = a;
+      if (j + 1 < cols) o[1] = b;
+      if (j + 2 < cols) o[2] = d;
+      if (j + 3 < cols) o[3] = e;
+    }
+  };
+  if constexpr (EPI == kEpiGated) {
+    const bool low = c < 2;  // has the gate values of both tiles; keeps the first
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float other = __shfl_xor(low ? acc[1][r] : acc[0][r], 32);
+      v[r] = activate(low ? acc[0][r] : other, epi.act) * (low ? other : acc[1][r]);
+    }
+    if (ok) put(epi.F, wt * 16 + (low ? 0 : 8) + 4 * (c & 1), v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = activate(acc[w][r], epi.act);
+      if (ok) put(g.N, wt * 32 + 16 * w + 4 * c, v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
 // Out through a transpose in the wavefront's own 32 x 20 floats of LDS, 16 columns at a time: four lanes
 // to a row's 64 bytes. A row's address is its pair's.
 template <class F, int TT, int EPI>
@@ -491,16 +631,13 @@ __device__ __forceinline__ void store(float* reg, const int2* rows, const Args& 
   }
 }
 
-template <class F, int EPI>
-__global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, EpiParam<EPI> epi) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  static_assert(F::BM <= 64 * F::NW, "a work-item per row");
+// A tile with its rows found, in parts of 32 rows or (FEW) as one of 16: two copies of all that follows, since
+// the compiler keeps the registers of code that both would share through either.
+template <class F, int EPI, bool FEW>
+__device__ __forceinline__ void tile(uint8_t* smem, const Args& g, const Pick& t, int2 row,
+                                     const EpiParam<EPI>& epi) {
   const int tid = threadIdx.x;
   int2* rows = reinterpret_cast<int2*>(smem + F::kRowsAt);
-  const Pick t = find_tile<F>(*reinterpret_cast<SearchLds*>(smem), g);
-  if (t.rows <= 0) return;
-  int2 row;
-  if (tid < F::BM) row = load_row<F>(g, t);
   Loads<F> ld;
   ld.init(smem, g);
   ld.aim(g, t);
@@ -512,7 +649,7 @@ __global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, E
   v4i raw[4];
   if (any) {  // the weights while the rows are on their way
 #pragma unroll
-    for (int gi = 0; gi < 4; ++gi) raw[gi] = ld.nibbles(s0, gi);
+    for (int gi = 0; gi < 4; ++gi) raw[gi] = FEW ? ld.nibbles16(s0, gi) : ld.nibbles(s0, gi);
   }
   if (tid < F::BM) rows[tid] = row;
   __syncthreads();
@@ -523,44 +660,64 @@ __global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, E
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  auto run = [&](auto parts) {
-    constexpr int TT = decltype(parts)::value;
-    v16f acc[TT];
-    sums<F, TT>(smem, ld, s0, s1, steps, raw, acc);
+  // The other ranges' sums, [range][wavefront][register][lane], added in the order of the ranges; whether
+  // this wavefront has them then.
+  auto join = [&](auto& acc) -> bool {
+    constexpr int V = sizeof(acc[0]) / 4, N = sizeof(acc) / 4;
     if constexpr (F::KS > 1) {
-      // the other ranges' sums, [range][wavefront][part][register][lane], added in the order of the
-      // ranges
-      static_assert((F::KS - 1) * F::CW * TT * 4096 <= 2 * F::kStage, "LDS of the sums");
+      static_assert((F::KS - 1) * F::CW * N * 256 <= 2 * F::kStage, "LDS of the sums");
       float* red = reinterpret_cast<float*>(smem) + ld.lane;
       if (ks > 0) {
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            red[((((ks - 1) * F::CW + ld.cw) * TT + u) * 16 + r) * 64] = acc[u][r];
+        for (int r = 0; r < N; ++r) red[(((ks - 1) * F::CW + ld.cw) * N + r) * 64] = acc[r / V][r % V];
       }
       __syncthreads();
-      if (ks > 0) return;
+      if (ks > 0) return false;
 #pragma unroll
       for (int o = 0; o < F::KS - 1; ++o)
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            acc[u][r] += red[(((o * F::CW + ld.cw) * TT + u) * 16 + r) * 64];
+        for (int r = 0; r < N; ++r) acc[r / V][r % V] += red[((o * F::CW + ld.cw) * N + r) * 64];
     }
-    // through the wavefront's region of weight scales
-    store<F, TT, EPI>(reinterpret_cast<float*>(smem + 2 * F::kStage + ld.wave * F::kExpanded), rows, g,
-                      t.tn * F::CW + ld.cw, ld.lane, acc, epi);
+    return true;
   };
-  using std::integral_constant;
-  if constexpr (F::TMAX == 4) {
-    if (ld.parts == 4) return run(integral_constant<int, 4>{});
-    if (ld.parts == 3) return run(integral_constant<int, 3>{});
-    if (ld.parts == 2) return run(integral_constant<int, 2>{});
+  const int wt = t.tn * F::CW + ld.cw;
+  if constexpr (FEW) {
+    v4f acc[2];
+    sums16<F>(smem, ld, s0, s1, steps, raw, acc);
+    if (join(acc)) store16<EPI>(rows, g, wt, ld.lane, acc, epi);
+  } else {
+    auto run = [&](auto parts) {
+      constexpr int TT = decltype(parts)::value;
+      v16f acc[TT];
+      sums<F, TT>(smem, ld, s0, s1, steps, raw, acc);
+      if (!join(acc)) return;
+      // through the wavefront's region of weight scales
+      store<F, TT, EPI>(reinterpret_cast<float*>(smem + 2 * F::kStage + ld.wave * F::kExpanded), rows,
+                        g, wt, ld.lane, acc, epi);
+    };
+    using std::integral_constant;
+    if constexpr (F::TMAX == 4) {
+      if (ld.parts == 4) return run(integral_constant<int, 4>{});
+      if (ld.parts == 3) return run(integral_constant<int, 3>{});
+      if (ld.parts == 2) return run(integral_constant<int, 2>{});
+    }
+    static_assert(F::TMAX == 1 || F::TMAX == 4, "the numbers of parts");
+    run(integral_constant<int, 1>{});
   }
-  static_assert(F::TMAX == 1 || F::TMAX == 4, "the numbers of parts");
-  run(integral_constant<int, 1>{});
+}
+
+template <class F, int EPI>
+__global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, EpiParam<EPI> epi) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  static_assert(F::BM <= 64 * F::NW, "a work-item per row");
+  const Pick t = find_tile<F>(*reinterpret_cast<SearchLds*>(smem), g);
+  if (t.rows <= 0) return;
+  int2 row = make_int2(-1, 0);
+  if ((int)threadIdx.x < F::BM) row = load_row<F>(g, t);
+  if constexpr (F::TMAX == 1) {
+    if (t.rows <= 16) return tile<F, EPI, true>(smem, g, t, row, epi);
+  }
+  tile<F, EPI, false>(smem, g, t, row, epi);
 }
 
 template <class F, int EPI>
