@@ -48,6 +48,12 @@ struct Form {
   static constexpr int TMAX = TMAX_, CW = CW_, KS = KS_, NW = CW_ * KS_, WAVES = WAVES_;
   static constexpr int BM = 32 * TMAX;
   static constexpr bool kLean = WAVES >= 4;  // 128 registers to a wavefront
+  // Weight-tile groups that an expert's tiles are gone through with before the next expert's: with 8 the
+  // narrow form takes 2 to 4 % less (777 tokens, 6 of 64, 1280 -> 2048: 84.0 -> 80.8 us) from its rows
+  // being in the L2; with 1 the wide form's short tiles, the last ones of the experts, are spread evenly
+  // over the XCDs (2048 tokens, 2 of 8: 11008 -> 4096 626 against 677 us with 8, 4096 -> 22016 1097
+  // against 1086).
+  static constexpr int kBlock = kLean ? 8 : 1;
   // One stage: per range of K the int8 token tile [BM][272], the (da, nb) pairs [4][BM][2 blocks][2]
   // and the token pieces [3][BM][8]; then the wavefronts' 32 row headers. Behind the two stages the
   // expanded weight scales, which only their wavefront uses, one super-block at a time; then the
@@ -126,21 +132,24 @@ __device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
     all += v;
   }
   all = min(all, g.most);  // what the grid covers (offsets of nonsense may ask for more)
-  // tiles in the order (weight-tile group, expert, rows), one contiguous range per XCD
+  // tiles in the order (weight-tile group's block, expert, group, rows), one contiguous range per XCD
   const unsigned total = (unsigned)all * (unsigned)g.gn;
   const unsigned per_xcd = (total + 7u) >> 3;
   const unsigned k = blockIdx.x >> 3;
   const unsigned idx = (blockIdx.x & 7u) * per_xcd + k;
   if (k < per_xcd && idx < total) {
-    const int tn = (int)(idx / (unsigned)all);
-    const int at = (int)(idx - (unsigned)tn * (unsigned)all);
+    const int block = (int)(idx / (unsigned)(all * F::kBlock));
+    const int at = (int)(idx - (unsigned)block * (unsigned)(all * F::kBlock));
+    const int wide = min(F::kBlock, g.gn - block * F::kBlock);  // groups of this block
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int mine = (n[c] + F::BM - 1) / F::BM;
-      const int u = at - (incl[c] - mine);
-      if (u >= 0 && u < mine)
+      const int local = at - (incl[c] - mine) * wide;
+      if (local >= 0 && local < mine * wide) {
+        const int tn = local / mine, u = local - tn * mine;
         sh.pick = Pick{(wave + c * F::NW) * 64 + lane, lo[c] + u * F::BM,
-                       min(n[c] - u * F::BM, F::BM), tn};
+                       min(n[c] - u * F::BM, F::BM), block * F::kBlock + tn};
+      }
     }
   }
   __syncthreads();
@@ -316,10 +325,13 @@ __device__ __forceinline__ void sums(uint8_t* smem, const Loads<F>& ld, int s0, 
         const int b = n / TT, t = n % TT;
         return *reinterpret_cast<const v4i*>(sArow + t * 32 * kRowStride + b * 32);
       };
+      float2 odd[TT];  // of the second block, read with the first's
       auto da_of = [&](int n) -> float2 {
         const int b = n / TT, t = n % TT;
-        return *reinterpret_cast<const float2*>(sDa + ((b >> 1) * F::BM + t * 32 + l32) * 16 +
-                                                (b & 1) * 8);
+        if (b & 1) return odd[t];
+        const float4 v = *reinterpret_cast<const float4*>(sDa + ((b >> 1) * F::BM + t * 32 + l32) * 16);
+        odd[t] = make_float2(v.z, v.w);
+        return make_float2(v.x, v.y);
       };
       auto dsv_of = [&](int b, float (&d)[16]) {
 #pragma unroll
@@ -443,6 +455,7 @@ __device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0
       q4k_stage_scales(hdr, lane & 31, lane >= 32, sW);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
+      float4 da2;
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         if (b % 2 == 0) set_priority(3 - b / 2);
@@ -457,7 +470,8 @@ __device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0
         }
         uint2 tok = *reinterpret_cast<const uint2*>(sArow + b * 32);
         asm volatile("" : "+v"(tok.x), "+v"(tok.y));  // the steps stay in order
-        const float2 da = *reinterpret_cast<const float2*>(sDa + (b >> 1) * F::BM * 16 + (b & 1) * 8);
+        if (b % 2 == 0) da2 = *reinterpret_cast<const float4*>(sDa + (b >> 1) * F::BM * 16);
+        const float2 da = b % 2 == 0 ? make_float2(da2.x, da2.y) : make_float2(da2.z, da2.w);
         const long top = __builtin_bit_cast(long, tok);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
