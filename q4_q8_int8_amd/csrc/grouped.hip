@@ -3,9 +3,8 @@
 //
 // The arithmetic is the tile of mmq_gemm.hip, per element the same operations in the same order (its
 // comment has the mathematics: one int8 MFMA per 32-block, two FMAs per element to rescale it, term2
-// on the bf16 unit, three instructions per super-block), so one expert that has all rows gives the
-// plain product's bits. It is bound as that kernel is, by the rescale's vector instructions. What
-// differs is which rows a workgroup has and how they get into LDS:
+// on the bf16 unit, three instructions per super-block). What differs is which rows a workgroup has and how
+// they get into LDS:
 //
 // - The host knows the pairs, not how they fall on the experts. The grid covers the most tiles that
 //   they can form (P / BM + min(E, P) for tiles of BM rows); a workgroup finds its expert and rows
@@ -13,14 +12,26 @@
 //   where there is no such tile.
 // - An expert's rows are cut into tiles of 32 TT rows, the last one of the 32-row parts it needs: the
 //   tile's code exists for 1 .. TT parts and a workgroup branches to its own, so a tile of few rows
-//   does not pay for the rescale of many.
+//   does not pay for the rescale of many. In the forms of 32 rows a tile of at most 16 uses 16 x 16
+//   instructions, half the elements to rescale (experts of 12 rows each, 22016 x 4096, 8 of them: 114 ->
+//   106 us; 2048 x 2048, 64 of them: 44.9 -> 43.9; no difference above 16).
 // - The rows are gathered by the loads into LDS: each lane's address has its row's place in the q8
 //   buffer, taken from the groups once per workgroup. quantize_q8_1's (da, nda) plane is block-major
-//   for contiguous rows; here it is row-major, 16 bytes holding two blocks of a row, and is staged as
-//   [4 pairs of blocks][BM] of 16 bytes. (Its 8-byte reads then meet two ways in the LDS banks, one
-//   read per 33 vector instructions.) Tokens are quantized once, not once per slot.
+//   for contiguous rows; here it is row-major, 16 bytes holding two blocks of a row, staged as
+//   [4 pairs of blocks][BM] of 16 bytes and read as one (read as two halves of 8 bytes, they met two ways in
+//   the LDS banks: 2048 tokens, 2 of 8, 1090 and 633 us against 1069 and 621). Tokens are quantized once,
+//   not once per slot.
 // - Workgroups go to the XCDs in turn. Each XCD gets a contiguous range of the tiles in the order
-//   (weight-tile group, expert, rows), so the row tiles that share weights run on one L2.
+//   (block of weight-tile groups, expert, group, rows), so the row tiles that share weights run on one L2.
+//
+// With few rows per expert it is bound by the weights' bytes: 64 experts, 100 tokens of 8 slots, D = 2048,
+// F = 1024 move their 151 MB of gate and up weights in 40 us with the quantization (3.8 TB/s, a large copy
+// moving 5.2; VALU 64 % busy). With many it is bound as the plain product is, by the rescale's vector
+// instructions: 2048 tokens, 2 of 8, 4096 -> 2 x 11008, 1072 us, 344 GMAC/ms, VALU 93 % busy (the plain
+// product reaches 377). Its clock is then 1.45 to 1.6 GHz by the power that the card allows, against 2.0 to
+// 2.1 in a single launch, which neither a longer pipeline (a workgroup that walks several tiles, with the
+// next one's first stage under the last super-block: 138 -> 139 us on 64 experts of 64 rows) nor other
+// tiles (64 rows, 4 or 8 wavefronts, 12 wavefronts on three SIMD slots: within 3 %) get past.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -758,7 +769,7 @@ hipError_t launch_t(const void* q8, const int* groups, const void* w, float* out
   return hipGetLastError();
 }
 
-// The forms of the kernel, and what a workgroup of each takes: fixed microseconds, and per super-block.
+// The forms of the kernel.
 using Wide = Form<4, 8, 1, 2>;   // 128 rows x 256 weight rows, one workgroup to a compute unit
 using Narrow = Form<1, 4, 1, 4>; // 32 x 128, four
 using Split2 = Form<1, 4, 2, 4>; // 32 x 128, K in two ranges, two
@@ -793,6 +804,19 @@ GroupedForm grouped_form(const GroupedShape& g, int64_t compute_units) {
   };
   const double wide = t128 * std::ceil(ntiles / 8.0), narrow = t32 * std::ceil(ntiles / 4.0);
   const double load = narrow / cus;
+  // What a form takes: rounds of its grid, times a workgroup's microseconds per super-block and its fixed ones
+  // (search, gather, first loads, store). Measured in every form (us, wide / narrow / two ranges of K / four;
+  // graph replays, quantization included), the choice being the best one or as said:
+  //   gated, 64 experts, 8 slots, D = 2048, F = 1024:  100 tokens 56 / 49 / 53 / 65, 512 111 / 99 / 106 /
+  //     142, 2048 254 / 286 / 307 / 407 (chosen: 258)
+  //   gated, 8 experts, 2 slots, D = 4096, F = 5504:   80 tokens 88 / 67 / 74 / 85, 500 203 / 204 / 212 / 248
+  //   gated, 16 experts, 2 slots, 2048, 1024:          20 tokens 24 / 22 / 18 / 18, 4000 (D = 1024) 94 / 92 /
+  //     109 / 153
+  //   plain, 8 experts, 300 tokens of 2, 4096 -> 1376: 87 / 43 / 32 / 28
+  //   down, 8 experts, 2 slots, 5632 -> 4096:          24 tokens 51 / 47 / 34 / 33, 80 67 / 57 / 46 / 52,
+  //     500 133 / 138 / 138 / 144 (chosen: 131)
+  //   down, 64 experts, 8 slots, 1024 -> 2048:         100 tokens 41 / 38 / 41 / 52, 2048 206 / 220 / 246 /
+  //     335 (chosen: narrow, the furthest of 36 shapes from their best, 7 %; the others are within 3 %)
   const double cost[4] = {
       rounds(wide, cus) * (nsb * (1.0 + 0.95 * t32 / t128) + 13.0),
       rounds(narrow, 4.0 * cus) * (nsb * us(load) + 5.0),

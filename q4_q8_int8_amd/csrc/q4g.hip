@@ -19,8 +19,12 @@
 // LDS, in the order of the wavefronts: a barrier for every tile costs as much as a tile's loads. A
 // wavefront brings the values of x for its own records into LDS with its first tile, in the form of the
 // operands: read from memory for every tile they take more of the vector memory unit than the weights do,
-// and their latency is not covered. Beside the loads, unpacking counts: 9 vector instructions per 8 values
-// for f16 and 8 for bf16.
+// and their latency is not covered (16 tokens, 11008 x 4096: 16.3 us in a graph, 11.5 from LDS). Beside the
+// loads, unpacking counts: 9 vector instructions per 8 values for f16 and 8 for bf16.
+//
+// Graph replays over weights beyond the caches, a launch being 3.6 us of each: 1 x 4096 x 4096 f16 5.1 us (9 MB),
+// 1 x 4096 x 11008 f32 with groups of 32 and zeros 11.1 (28 MB), 16 x 11008 x 4096 bf16 11.4 (24 MB),
+// 1 x 22016 x 4096 bf16 13.1 (48 MB): 3.1 to 6 TB/s beyond the launch, VALU 33 to 54 % busy.
 #include <algorithm>
 
 #include "epilogue.h"
@@ -396,16 +400,21 @@ Plan plan(int x_type, int64_t M, const Q4GShape& g, int64_t cus) {
   constexpr int64_t kLds = 160 << 10;
   Plan p;
   const int q = token_groups(M);
-  // 8 wavefronts instead of 16: where less than half of the compute units have a tile, and, two workgroups
-  // to a unit, where every unit has several and a tile's sums are few.
+  // 8 wavefronts instead of 16 where half of the compute units or fewer have a tile (graph replays, 8 against
+  // 16: 1 x 1024 x 4096 f16 4.6 and 4.8 us, 3 x 1376 x 4096 bf16 4.7 and 5.0, 1 x 2048 x 4096 4.8 and 4.9, but
+  // 1 x 3000 x 4096 5.0 and 4.9, 1 x 4096 x 4096 5.3 and 5.1), and, as two workgroups to a unit, where every
+  // unit has several tiles and a tile's sums are few (1 x 8192 x 4096 7.0 and 7.1, 1 x 11008 x 4096 8.5 and
+  // 8.8, 1 x 22016 x 4096 13.1 and 13.4; float32 9.8 and 9.4, 9 tokens 10.0 and 9.8).
   const bool several = g.tiles() >= 2 * cus && q == 1 && x_type != kTypeF32;
   const int64_t per = several ? 2 : 1;
-  p.nw = several || 2 * g.tiles() < cus ? 8 : max_waves(x_type, q);
+  p.nw = several || 2 * g.tiles() <= cus ? 8 : max_waves(x_type, q);
   while (p.nw > 1 && p.nw > g.records()) p.nw /= 2;
   p.grid = std::min(g.tiles(), per * cus);
   const int64_t row = p.nw * x_rows(x_type, M) * kRowBytes, sums = p.nw * q * 256;
   p.slots = (g.records() + p.nw - 1) / p.nw;
   // one tile: float32 values on their way into LDS between the records, not all before the first
+  // (1 x 4096 x 11008 11.1 us against 11.8, 1 x 4096 x 4096
+  // 5.0 against 5.6)
   p.all = p.slots * row + sums <= kLds / per && (x_type != kTypeF32 || g.tiles() > cus);
   if (!p.all) p.slots = 1;
   const int64_t most = (g.tiles() + p.grid - 1) / p.grid;
