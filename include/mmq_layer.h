@@ -224,7 +224,7 @@ int mmq_moe_group(int64_t M, int64_t E, int64_t k, const int32_t* ids, int32_t* 
  * 8, 4096, 11008: 85 and 43 against 100 and 49), and where an expert gets some 4 to 8 of the pairs on
  * average the two meet (64 tokens: 45 and 37 against 39 and 29; 128 and 76 against 109 and 54).
  * K % 256 == 0, K <= 2^24, (rows of x)*K < 2^31, N <= 2^30, and (M*k/32 + min(E, M*k)) * ceil(N/256)
- * < 2^23 - 8 (gated: of its 32 * ceil(F/16) packed rows).
+ * < 2^23 - 4096 (gated: of its 32 * ceil(F/16) packed rows).
  * Errors: MMQ_E_ARG, MMQ_E_SHAPE, MMQ_E_LDS, MMQ_E_DEVICE, MMQ_E_HIP.
  */
 int mmq_q4K_grouped(int64_t M, int64_t E, int64_t k, int64_t N, int64_t K, const float* x,

@@ -65,6 +65,8 @@ struct Form {
   // over the XCDs (2048 tokens, 2 of 8: 11008 -> 4096 626 against 677 us with 8, 4096 -> 22016 1097
   // against 1086).
   static constexpr int kBlock = kLean ? 8 : 1;
+  // Whether the last round of an XCD's tiles is cut finer (find_tile).
+  static constexpr bool kTail = TMAX == 4;
   // One stage: per range of K the int8 token tile [BM][272], the (da, nb) pairs [4][BM][2 blocks][2]
   // and the token pieces [3][BM][8]; then the wavefronts' 32 row headers. Behind the two stages the
   // expanded weight scales, which only their wavefront uses, one super-block at a time; then the
@@ -93,6 +95,7 @@ struct Args {
   float* out;
   int P, E, N, K, q_rows, per_row, gn, order_at;
   int most;  // the most tiles of a weight-tile group that the pairs can form
+  int slots; // workgroups that an XCD runs at a time (F::kTail)
 };
 
 // A tile: its expert, its first row in the order, its rows (0: none) and its weight-tile group.
@@ -146,7 +149,22 @@ __device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
   // tiles in the order (weight-tile group's block, expert, group, rows), one contiguous range per XCD
   const unsigned total = (unsigned)all * (unsigned)g.gn;
   const unsigned per_xcd = (total + 7u) >> 3;
-  const unsigned k = blockIdx.x >> 3;
+  unsigned k = blockIdx.x >> 3;
+  // The tiles of an XCD's last round, where they fill a half or a quarter of it, as 2 or 4 workgroups of 64 or
+  // 32 rows each (1500 tokens, 2 of 8: 4096 -> 2 x 4096 345 -> 322 us, 4096 -> 4096 213.5 and 214.8; 2048 tokens,
+  // 4096 -> 2 x 11008 1106 -> 1099, 11008 -> 4096 630 -> 626; cut so everywhere a tile's weights would be
+  // expanded and its rows' scales read four times).
+  int part = 0, shift = 0;
+  if constexpr (F::kTail) {
+    const unsigned last = per_xcd % (unsigned)g.slots, whole = per_xcd - last;
+    shift = 4 * last <= (unsigned)g.slots ? 2 : 2 * last <= (unsigned)g.slots ? 1 : 0;
+    if (k >= whole) {
+      part = (int)((k - whole) & ((1u << shift) - 1u));
+      k = whole + ((k - whole) >> shift);
+    } else {
+      shift = 0;
+    }
+  }
   const unsigned idx = (blockIdx.x & 7u) * per_xcd + k;
   if (k < per_xcd && idx < total) {
     const int block = (int)(idx / (unsigned)(all * F::kBlock));
@@ -158,8 +176,9 @@ __device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
       const int local = at - (incl[c] - mine) * wide;
       if (local >= 0 && local < mine * wide) {
         const int tn = local / mine, u = local - tn * mine;
-        sh.pick = Pick{(wave + c * F::NW) * 64 + lane, lo[c] + u * F::BM,
-                       min(n[c] - u * F::BM, F::BM), block * F::kBlock + tn};
+        const int row = u * F::BM + part * (F::BM >> shift);
+        sh.pick = Pick{(wave + c * F::NW) * 64 + lane, lo[c] + row,
+                       min(n[c] - row, F::BM >> shift), block * F::kBlock + tn};
       }
     }
   }
@@ -747,7 +766,7 @@ __global__ __launch_bounds__(F::NW * 64, F::WAVES) void grouped_kernel(Args g, E
 
 template <class F, int EPI>
 hipError_t launch_t(const void* q8, const int* groups, const void* w, float* out,
-                    const GroupedShape& g, const Epilogue& epi, hipStream_t s) {
+                    const GroupedShape& g, const Epilogue& epi, int64_t cus, hipStream_t s) {
   const uint8_t* base = static_cast<const uint8_t*>(q8);
   auto kern = grouped_kernel<F, EPI>;
   if (F::kLds > 65536) {
@@ -757,13 +776,14 @@ hipError_t launch_t(const void* q8, const int* groups, const void* w, float* out
   }
   const int64_t gn = ((g.N + 31) / 32 + F::CW - 1) / F::CW;
   const int64_t most = g.P / F::BM + (g.E < g.P ? g.E : g.P);
-  const int64_t grid = (most * gn + 7) / 8 * 8;
+  const int64_t slots = std::max<int64_t>(1, cus / 8);
+  const int64_t grid = ((most * gn + 7) / 8 + (F::kTail ? slots : 0)) * 8;
   const Args a{reinterpret_cast<const int8_t*>(base),
                reinterpret_cast<const float*>(base + q8_planes_offset(g.q_rows, g.K)),
                reinterpret_cast<const uint16_t*>(base + q8_pieces_offset(g.q_rows, g.K)),
                groups, static_cast<const uint8_t*>(w), out, (int)g.P, (int)g.E, (int)g.N, (int)g.K,
                (int)g.q_rows, (int)g.per_row, (int)gn, (int)GroupLayout{g.P, g.E}.order(),
-               (int)most};
+               (int)most, (int)slots};
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * F::NW), (size_t)F::kLds, s, a,
                      epi_param<EPI>(epi));
   return hipGetLastError();
@@ -779,10 +799,10 @@ template <int EPI>
 hipError_t launch_epi(const void* q8, const int* groups, const void* w, float* out,
                       const GroupedShape& g, const Epilogue& epi, int64_t cus, hipStream_t s) {
   switch (grouped_form(g, cus)) {
-    case kGroupedNarrow: return launch_t<Narrow, EPI>(q8, groups, w, out, g, epi, s);
-    case kGroupedSplit2: return launch_t<Split2, EPI>(q8, groups, w, out, g, epi, s);
-    case kGroupedSplit4: return launch_t<Split4, EPI>(q8, groups, w, out, g, epi, s);
-    default: return launch_t<Wide, EPI>(q8, groups, w, out, g, epi, s);
+    case kGroupedNarrow: return launch_t<Narrow, EPI>(q8, groups, w, out, g, epi, cus, s);
+    case kGroupedSplit2: return launch_t<Split2, EPI>(q8, groups, w, out, g, epi, cus, s);
+    case kGroupedSplit4: return launch_t<Split4, EPI>(q8, groups, w, out, g, epi, cus, s);
+    default: return launch_t<Wide, EPI>(q8, groups, w, out, g, epi, cus, s);
   }
 }
 

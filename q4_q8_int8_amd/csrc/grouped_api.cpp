@@ -51,11 +51,11 @@ int check_product(int64_t M, int64_t E, int64_t k, const char* rows_name, int64_
     return fail(MMQ_E_SHAPE, "activations of %lld x %lld: 2^31 values or more", (long long)q_rows,
                 (long long)K);
   const int64_t N = gated ? mmq::pair_rows(rows) : rows;
-  // Workgroups of 256 work-items on 32 x 128 tiles or 512 on 128 x 256: below 2^32 work-items, the
-  // workgroups rounded up to a multiple of 8 (the split forms' grids are smaller, grouped_form).
+  // Workgroups of 256 work-items on 32 x 128 tiles or 512 on 128 x 256: below 2^32 work-items, with a
+  // round of them more (grouped.hip; the split forms' grids are smaller, grouped_form).
   const int64_t P = M * k, tiles = P / 32 + (E < P ? E : P);
-  if (tiles * ((N + 255) / 256) >= ((int64_t)1 << 23) - 8)
-    return fail(MMQ_E_SHAPE, "M*k = %lld, E = %lld, %s = %lld: 2^23 - 8 tiles or more",
+  if (tiles * ((N + 255) / 256) >= ((int64_t)1 << 23) - 4096)
+    return fail(MMQ_E_SHAPE, "M*k = %lld, E = %lld, %s = %lld: 2^23 - 4096 tiles or more",
                 (long long)P, (long long)E, rows_name, (long long)rows);
   return MMQ_OK;
 }

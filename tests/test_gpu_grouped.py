@@ -204,6 +204,78 @@ def test_every_form(form, M, E, k, N, K):
     assert bool(torch.isnan(C[torch.from_numpy(np.nonzero(flat == E)[0]).cuda()]).all())
 
 
+# tiles of an XCD (32 compute units each): 8, 28, 38, 40, 44, 52, 54, 64, 68, 75: none, a few, some and most in
+# its last round, whose tiles are cut finer where they are few
+@pytest.mark.parametrize("rows,N", [(100, 8192), (700, 8192), (1100, 7500), (1152, 8192), (1280, 8192),
+                                    (1536, 8192), (1535, 8330), (1920, 8192), (2048, 8192), (2049, 8400)])
+def test_wide_forms_last_round(rows, N):
+    """One expert with most rows and a ragged one, against the plain product bit for bit."""
+    E, K = 2, 2048
+    counts = (rows, 45)
+    assert gu.grouped_form(4096, E, N, K) == "wide"
+    ids = np.full((4096, 1), -1, np.int32)
+    at = np.random.default_rng(rows).permutation(4096)
+    ids[at[:rows]], ids[at[rows:rows + 45]] = 0, 1
+    x = to_dev(synth.activations("normal_outliers", 4096, K, N))
+    blocks = to_dev(synth.q4k_weights("random_fields", E * N, K, 3)[0]).reshape(E, -1)
+    n = mmq.mmq_q4K_repacked_bytes(N, K)
+    rep = raw(E * n)
+    for e in range(E):
+        mmq.repack_q4_K(blocks[e], N, K, rep[e * n:(e + 1) * n])
+    C = f32(4096, N)
+    say("grouped wide", counts, N, "tiles", -(-rows // 128) + 1, "by", -(-N // 256))
+    mmq.mmq_q4K_grouped(4096, E, 1, N, K, x, group(ids, E), rep, C, raw(mmq.mmq_q8_1_bytes(4096, K)))
+    for e in range(E):
+        ps = torch.from_numpy(np.nonzero(ids.reshape(-1) == e)[0]).cuda()
+        assert len(ps) == counts[e]
+        assert torch.equal(C[ps], plain_rows(x[ps].contiguous(), rep, e, n, N, K)), e
+    none = torch.from_numpy(np.nonzero(ids.reshape(-1) < 0)[0]).cuda()
+    assert bool(torch.isnan(C[none]).all())
+
+
+def test_tokens_of_nan_and_infinity_stay_alone():
+    """In every form: the other pairs' rows are bit for bit what they are without them."""
+    for form, M, E, k, N, K in FORMS:
+        assert gu.grouped_form(M * k, E, N, K) == form
+        ids = np.random.default_rng(2).integers(0, E, (M, k)).astype(np.int32)
+        x = to_dev(synth.activations("normal_outliers", M, K, N))
+        n = mmq.mmq_q4K_repacked_bytes(N, K)
+        rep = raw(E * n)
+        blocks = synth.q4k_weights("random_fields", N, K, 3)[0]
+        for e in range(E):
+            mmq.repack_q4_K(to_dev(blocks), N, K, rep[e * n:(e + 1) * n])
+        g, q8 = group(ids, E), raw(mmq.mmq_q8_1_bytes(M, K))
+        clean, C = f32(M * k, N), f32(M * k, N)
+        say("grouped with NaN", form)
+        mmq.mmq_q4K_grouped(M, E, k, N, K, x, g, rep, clean, q8)
+        assert bool(torch.isfinite(clean).all())
+        x[3, 7], x[M - 1, K - 1], x[11, 300] = NAN, float("inf"), -float("inf")
+        mmq.mmq_q4K_grouped(M, E, k, N, K, x, g, rep, C, q8)
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[[3, 11, M - 1]] = False
+        keep = keep.repeat_interleave(k)
+        assert torch.equal(C[keep], clean[keep]), form
+
+
+@pytest.mark.parametrize("M,k", [(3, 2), (150, 2), (4000, 1)])
+def test_no_pair_has_an_expert(M, k):
+    E, D, F = 8, 256, 256
+    ids = np.full((M, k), -1, np.int32)
+    pairs, down = experts("pair", E, F, D, 700)[0], experts("plain", E, D, F, 800)[0]
+    g = group(ids, E)
+    x = to_dev(synth.activations("normal", M, D, 1))
+    H, out = f32(M * k, F), f32(M, D)
+    say("no experts", M, k)
+    mmq.mmq_q4K_grouped_gated(M, E, k, F, D, x, g, pairs, H, raw(mmq.mmq_q8_1_bytes(M, D)))
+    assert bool(torch.isnan(H).all())
+    space = raw(mmq.mmq_grouped_down_workspace_bytes(M, E, k, D, F))
+    wts = torch.ones(M, k, device="cuda")
+    mmq.mmq_q4K_grouped_down(M, E, k, D, F, H, g, wts, down, out, space)
+    assert not bool(out.any()) and bool(torch.isfinite(out).all())
+    mmq.mmq_q4K_grouped_down(M, E, k, D, F, H, g, wts, down, out, space, residual=x)
+    assert torch.equal(out, x)
+
+
 @pytest.mark.parametrize("act", lo.ACTS)
 def test_grouped_activation(act):
     k, N, K, E = 2, 100, 512, len(RAGGED)
