@@ -25,9 +25,9 @@
 //   (block of weight-tile groups, expert, group, rows), so the row tiles that share weights run on one L2.
 //
 // With few rows per expert it is bound by the weights' bytes: 64 experts, 100 tokens of 8 slots, D = 2048,
-// F = 1024 move their 151 MB of gate and up weights in 40 us with the quantization (3.8 TB/s, a large copy
-// moving 5.2; VALU 64 % busy). With many it is bound as the plain product is, by the rescale's vector
-// instructions: 2048 tokens, 2 of 8, 4096 -> 2 x 11008, 1072 us, 344 GMAC/ms, VALU 93 % busy (the plain
+// F = 1024 move their 151 MB of gate and up weights in 40 to 51 us with the quantization (3.0 to 3.8 TB/s, a
+// large copy moving 5.2; VALU 65 % busy). With many it is bound as the plain product is, by the rescale's vector
+// instructions: 2048 tokens, 2 of 8, 4096 -> 2 x 11008, 1056 us, 350 GMAC/ms, VALU 93 % busy (the plain
 // product reaches 377). Its clock is then 1.45 to 1.6 GHz by the power that the card allows, against 2.0 to
 // 2.1 in a single launch, which neither a longer pipeline (a workgroup that walks several tiles, with the
 // next one's first stage under the last super-block: 138 -> 139 us on 64 experts of 64 rows) nor other
@@ -152,7 +152,7 @@ __device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
   unsigned k = blockIdx.x >> 3;
   // The tiles of an XCD's last round, where they fill a half or a quarter of it, as 2 or 4 workgroups of 64 or
   // 32 rows each (1500 tokens, 2 of 8: 4096 -> 2 x 4096 345 -> 322 us, 4096 -> 4096 213.5 and 214.8; 2048 tokens,
-  // 4096 -> 2 x 11008 1106 -> 1099, 11008 -> 4096 630 -> 626; cut so everywhere a tile's weights would be
+  // 4096 -> 2 x 11008 1106 -> 1099, 11008 -> 4096 630 -> 626 and, of other counts, 636 -> 543; cut so everywhere a tile's weights would be
   // expanded and its rows' scales read four times).
   int part = 0, shift = 0;
   if constexpr (F::kTail) {
