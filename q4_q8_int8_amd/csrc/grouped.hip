@@ -26,11 +26,11 @@
 //
 // With few rows per expert it is bound by the weights' bytes: 64 experts, 100 tokens of 8 slots, D = 2048,
 // F = 1024 move their 151 MB of gate and up weights in 40 to 51 us with the quantization (3.0 to 3.8 TB/s, a
-// large copy moving 5.2; VALU 65 % busy). With many it is bound as the plain product is, by the rescale's vector
-// instructions: 2048 tokens, 2 of 8, 4096 -> 2 x 11008, 1056 us, 350 GMAC/ms, VALU 93 % busy (the plain
-// product reaches 377). Its clock is then 1.45 to 1.6 GHz by the power that the card allows, against 2.0 to
-// 2.1 in a single launch, which neither a longer pipeline (a workgroup that walks several tiles, with the
-// next one's first stage under the last super-block: 138 -> 139 us on 64 experts of 64 rows) nor other
+// large copy moving 5.2; VALU 65 % busy). With many it is bound as the plain product is, by the rescale's
+// vector instructions: 2048 tokens, 2 of 8, 4096 -> 2 x 11008, 1056 us, 350 GMAC/ms, VALU 93 % busy (the
+// plain product reaches 377). Its clock is then 1.45 to 1.6 GHz by the power that the card allows, against
+// 2.0 to 2.1 in a single launch, which neither a longer pipeline (a workgroup that walks several tiles, with
+// the next one's first stage under the last super-block: 138 -> 139 us on 64 experts of 64 rows) nor other
 // tiles (64 rows, 4 or 8 wavefronts, 12 wavefronts on three SIMD slots: within 3 %) get past.
 #include <algorithm>
 #include <cmath>
@@ -95,7 +95,7 @@ struct Args {
   float* out;
   int P, E, N, K, q_rows, per_row, gn, order_at;
   int most;  // the most tiles of a weight-tile group that the pairs can form
-  int slots; // workgroups that an XCD runs at a time (F::kTail)
+  int slots;  // workgroups that an XCD runs at a time (F::kTail)
 };
 
 // A tile: its expert, its first row in the order, its rows (0: none) and its weight-tile group.
@@ -152,8 +152,8 @@ __device__ __forceinline__ Pick find_tile(SearchLds& sh, const Args& g) {
   unsigned k = blockIdx.x >> 3;
   // The tiles of an XCD's last round, where they fill a half or a quarter of it, as 2 or 4 workgroups of 64 or
   // 32 rows each (1500 tokens, 2 of 8: 4096 -> 2 x 4096 345 -> 322 us, 4096 -> 4096 213.5 and 214.8; 2048 tokens,
-  // 4096 -> 2 x 11008 1106 -> 1099, 11008 -> 4096 630 -> 626 and, of other counts, 636 -> 543; cut so everywhere a tile's weights would be
-  // expanded and its rows' scales read four times).
+  // 4096 -> 2 x 11008 1106 -> 1099, 11008 -> 4096 630 -> 626 and, of other counts, 636 -> 543). Fuller rounds
+  // stay whole: finer workgroups unpack a tile's weights and expand its scales again, each for itself.
   int part = 0, shift = 0;
   if constexpr (F::kTail) {
     const unsigned last = per_xcd % (unsigned)g.slots, whole = per_xcd - last;
