@@ -44,6 +44,7 @@ namespace mmq {
 namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ void set_priority(int p) {
   if (p >= 3) __builtin_amdgcn_s_setprio(3);
@@ -456,7 +457,11 @@ __device__ __forceinline__ void sums(uint8_t* smem, const Loads<F>& ld, int s0, 
 }
 
 // The same for a tile of at most 16 rows: the 32 weight rows are two tiles of 16 x 16, half the elements to
-// rescale. Lane (r, c) has token r and, in acc[w], weight rows 16 w + 4 c .. + 3. raw as nibbles16.
+// rescale. Lane (r, c) has token r and, in acc[w], weight rows 16 w + 4 c .. + 3. raw as nibbles16. Every
+// element's operations are those of sums, in their order, so that a row's bits do not go by how many other
+// rows its tile has: term2 in the same three steps of 16 products, whose sum the 16 x 16 x 16 and the 32 x 32 x
+// 16 instruction round alike (the same bits in 25 million sums of exponents up to 2^+-60). 32 products at a time
+// round otherwise.
 template <class F>
 __device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0, int s1, int steps,
                                        v4i (&raw)[4], v4f (&acc)[2]) {
@@ -466,9 +471,8 @@ __device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0
   for (int r = 0; r < 4; ++r) bias[r] = kBiasBits;
   asm volatile("" : "+v"(bias));
   acc[0] = acc[1] = v4f{0.f, 0.f, 0.f, 0.f};
-  // term2's piece pairs (weights, tokens): (0, 0) (0, 1) (1, 0) (0, 2), then (1, 1) (2, 0)
-  const int ia = c == 2 ? 1 : 0, jb = c == 1 ? 1 : (c == 3 ? 2 : 0);
-  const int ib = c == 0 ? 1 : 2, jc = c == 0 ? 1 : 0;
+  // which half of a third's 16 products, two piece pairs of 8 blocks each, the lane holds four of
+  const int h = c >> 1, part = (c & 1) * 8;
   for (int i = 0; i < steps; ++i) {
     const int s = s0 + i, p = i & 1;
     const bool more = s + 1 < s1;
@@ -518,18 +522,16 @@ __device__ __forceinline__ void sums16(uint8_t* smem, const Loads<F>& ld, int s0
             acc[w][r] = __builtin_fmaf(__builtin_fmaf(__int_as_float(Dr), da.x, da.y), ds[r], acc[w][r]);
           }
         }
-        if (b == 1 || b == 3) {
-          const bool zero = b == 3 && c >= 2;
-          const int wi = b == 1 ? ia : ib, ti = b == 1 ? jb : jc;
-          v4i tb = *reinterpret_cast<const v4i*>(sTp + (ti * F::BM + r16) * 16);
-          if (zero) tb = v4i{0, 0, 0, 0};
+        if (b == 1 || b == 3 || b == 5) {  // a third of term2, as in sums
+          const int u = b >> 1;
+          const int ia = u == 0 ? 0 : (u == 1 ? 1 - h : 1 + h);
+          const int jb = u == 0 ? h : (u == 1 ? 2 * h : 1 - h);
+          const v4s tb = *reinterpret_cast<const v4s*>(sTp + (jb * F::BM + r16) * 16 + part);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            v4i wa =
-                *reinterpret_cast<const v4i*>(sW + kWDsvBytes + (wi * 32 + 16 * w + r16) * 16);
-            if (zero) wa = v4i{0, 0, 0, 0};
-            acc[w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(v8bf, wa), __builtin_bit_cast(v8bf, tb), acc[w], 0, 0, 0);
+            const v4s wa = *reinterpret_cast<const v4s*>(
+                sW + kWDsvBytes + (ia * 32 + 16 * w + r16) * 16 + part);
+            acc[w] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(wa, tb, acc[w], 0, 0, 0);
           }
         }
       }
