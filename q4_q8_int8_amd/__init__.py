@@ -768,11 +768,11 @@ def _q4G_bytes(N, K, group, scale_type, zeros, reserved):
 
 
 def _q4G_size(N, K, f):
-    return _q4G_bytes(_int(N), _int(K), f.group, f.scale_type, f.zeros, f.reserved)
+    return _q4G_bytes(N, K, f.group, f.scale_type, f.zeros, f.reserved)
 
 
 def mmq_q4G_repacked_bytes(N: int, K: int, format: mmq_q4G_format) -> int:
-    return _q4G_size(N, K, format)
+    return _q4G_size(_int(N), _int(K), format)
 
 
 def repack_q4_G(w, scales, zeros, N: int, K: int, format: mmq_q4G_format, w_rep,
@@ -780,6 +780,7 @@ def repack_q4_G(w, scales, zeros, N: int, K: int, format: mmq_q4G_format, w_rep,
     """w: uint8 [N, K/2], the even value of two in the low four bits; scales and zeros (None where the
     format has none): [N, ceil(K/group)] of the format's type; w_rep: mmq_q4G_repacked_bytes."""
     here = _here()
+    N, K = _int(N), _int(K)  # the sizes below in Python's integers, which do not wrap
     rn = _q4G_size(N, K, format)
     dtype = torch.float16 if format.scale_type == MMQ_F16 else torch.bfloat16
     n = 2 * N * -(-K // format.group)
@@ -796,6 +797,7 @@ def mmq_q4G(M: int, N: int, K: int, x, w_rep, format: mmq_q4G_format, y, bias=No
     """y[M, N] = act(x[M, K] W^T + bias[N]) + residual[M, N] for 1 <= M <= 16 tokens. x and y: float32,
     float16 or bfloat16 each; residual of y's type (it may be y), bias float32."""
     here = _here()
+    M, N, K = _int(M), _int(N), _int(K)
     rn = _q4G_size(N, K, format)
     xt, yt = TYPES.get(getattr(x, "dtype", None)), TYPES.get(getattr(y, "dtype", None))
     if xt is None or yt is None:
