@@ -384,13 +384,17 @@ def mmq_q4K_f32(M: int, N: int, K: int, x, w_rep, C, stream=None) -> None:
     _check("mmq_q4K_f32", _lib.mmq_q4K_f32(M, N, K, xp, rp, cp, _stream(stream, here)))
 
 
+def _dots_bytes(K, per, i0, i1, j0, j1) -> int:
+    return 4 * (_int(K) // per) * max(_int(i1) - _int(i0), 0) * max(_int(j1) - _int(j0), 0)
+
+
 def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, j0: int,
                            j1: int, S, stream=None, force_tile: int = MMQ_TILE_AUTO,
                            lds_budget: int = 0) -> None:
     """S: int32 device tensor [K/32, i1-i0, j1-j0] of per-block integer dot products."""
     qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
     rp = _dev(w_rep, "w_rep", _sized(mmq_q4K_repacked_bytes, N, K))
-    sp = _dev(S, "S", 4 * (K // QK8) * max(i1 - i0, 0) * max(j1 - j0, 0), torch.int32)
+    sp = _dev(S, "S", _dots_bytes(K, QK8, i0, i1, j0, j1), torch.int32)
     _check("mmq_q4K_q8_1_blockdots",
            _lib.mmq_q4K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp,
                                        _stream(stream), _opts(force_tile, lds_budget)))
@@ -398,6 +402,7 @@ def mmq_q4K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
 
 # ---------------------------------------------------------------- the product's epilogue
 def _epi(M: int, N: int, bias, residual, act: int, here: int):
+    M, N = _int(M), _int(N)
     bp = None if bias is None else _dev(bias, "bias", 4 * N, torch.float32, here)
     rp = None if residual is None else _dev(residual, "residual", 4 * M * N, torch.float32, here)
     return ctypes.byref(mmq_epilogue(bp, rp, act, 0))
@@ -501,7 +506,7 @@ def mmq_moe_plan_bytes(M: int, E: int, k: int) -> int:
 def mmq_moe_plan(M: int, E: int, k: int, ids, plan, stream=None) -> None:
     """plan (int32, mmq_moe_plan_bytes) from ids int32 [M, k]; an id outside [0, E) is no expert."""
     here = _here()
-    ip = _dev(ids, "ids", 4 * M * k, torch.int32, here)
+    ip = _dev(ids, "ids", 4 * _int(M) * _int(k), torch.int32, here)
     pp = _dev(plan, "plan", _sized(mmq_moe_plan_bytes, M, E, k), torch.int32, here)
     _check("mmq_moe_plan", _lib.mmq_moe_plan(M, E, k, ip, pp, _stream(stream, here)))
 
@@ -866,7 +871,7 @@ def mmq_q6K_q8_1_blockdots(M: int, N: int, K: int, q8, w_rep, i0: int, i1: int, 
     """S: int32 device tensor [K/16, i1-i0, j1-j0] of per-group integer dot products."""
     qp = _dev(q8, "q8", _sized(mmq_q8_1_bytes, M, K))
     rp = _dev(w_rep, "w_rep", _sized(mmq_q6K_repacked_bytes, N, K))
-    sp = _dev(S, "S", 4 * (K // 16) * max(i1 - i0, 0) * max(j1 - j0, 0), torch.int32)
+    sp = _dev(S, "S", _dots_bytes(K, 16, i0, i1, j0, j1), torch.int32)
     _check("mmq_q6K_q8_1_blockdots",
            _lib.mmq_q6K_q8_1_blockdots(M, N, K, qp, rp, i0, i1, j0, j1, sp, _stream(stream),
                                        _opts(force_tile)))
@@ -892,7 +897,7 @@ def mmq_f16_bytes(rows: int, K: int) -> int:
 
 def convert_f32_f16(x, M: int, K: int, x_f16, stream=None) -> None:
     """x: f32 [M, K] device tensor; x_f16: device buffer of mmq_f16_bytes(M, K) bytes."""
-    xp = _dev(x, "x", 4 * M * K, torch.float32)
+    xp = _dev(x, "x", 4 * _int(M) * _int(K), torch.float32)
     hp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
     _check("convert_f32_f16", _lib.convert_f32_f16(xp, M, K, hp, _stream(stream)))
 
@@ -908,7 +913,7 @@ def gemm_f16(M: int, N: int, K: int, x_f16, w_f16, C, stream=None) -> None:
     """C[M, N] (f32 device tensor) = x_f16 [M, K] times w_f16 [N, K]^T, f32 accumulation."""
     xp = _dev(x_f16, "x_f16", _sized(mmq_f16_bytes, M, K))
     wp = _dev(w_f16, "w_f16", _sized(mmq_f16_bytes, N, K))
-    cp = _dev(C, "C", 4 * M * N, torch.float32)
+    cp = _dev(C, "C", 4 * _int(M) * _int(N), torch.float32)
     _check("gemm_f16", _lib.gemm_f16(M, N, K, xp, wp, cp, _stream(stream)))
 
 

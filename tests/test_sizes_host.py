@@ -56,3 +56,49 @@ def test_q4g_sizes(kind, monkeypatch):
         assert want["bias"] == 4 * N
         assert needed(monkeypatch, "mmq_q4G", kind(M), kind(N), kind(K), *a, bias=0,
                       residual=0) == want
+
+
+# calls whose sizes are multiplied in the wrapper itself; the buffers that then need more than 2^31 bytes
+OTHERS = [
+    ("mmq_q4K_q8_1_epilogue", (1 << 15, 1 << 16, 256), ("residual",)),
+    ("mmq_q4K_f32_epilogue", (128, 1 << 25, 256), ("residual",)),
+    ("convert_f32_f16", (1 << 16, 1 << 14), ("x",)),
+    ("gemm_f16", (1 << 15, 1 << 16, 256), ("C",)),
+]
+
+
+@pytest.mark.filterwarnings("ignore:overflow encountered")
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fn,sizes,large", OTHERS)
+def test_sizes_of_the_other_calls(fn, sizes, large, kind, monkeypatch):
+    rest = {"mmq_q4K_q8_1_epilogue": 3, "mmq_q4K_f32_epilogue": 3, "convert_f32_f16": 0,
+            "gemm_f16": 3}[fn]
+    args = (0,) * rest
+    kw = dict(bias=0, residual=0) if "epilogue" in fn else {}
+    if fn == "convert_f32_f16":     # x comes before the sizes
+        call = lambda t: needed(monkeypatch, fn, 0, *map(t, sizes), 0)
+    else:
+        call = lambda t: needed(monkeypatch, fn, *map(t, sizes), *args, **kw)
+    want = call(int)
+    assert all(want[b] >= 2 ** 31 for b in large), want
+    assert call(kind) == want
+
+
+@pytest.mark.filterwarnings("ignore:overflow encountered")
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fn,per", [("mmq_q4K_q8_1_blockdots", 32), ("mmq_q6K_q8_1_blockdots", 16)])
+def test_sizes_of_the_block_dots(fn, per, kind, monkeypatch):
+    M, N, K, rows, cols = 4096, 8192, 4096, 4096, 8192
+    call = lambda t: needed(monkeypatch, fn, *map(t, (M, N, K)), 0, 0, t(0), t(rows), t(0), t(cols),
+                            0)
+    want = call(int)
+    assert want["S"] == 4 * (K // per) * rows * cols
+    assert call(kind) == want
+
+
+def test_size_of_a_plans_ids(monkeypatch):
+    """(A plan's sizes fit any integer of 16 bits and more.)"""
+    want = needed(monkeypatch, "mmq_moe_plan", 64, 512, 8, 0, 0)
+    assert want["ids"] == 4 * 64 * 8
+    for kind in (np.int8, np.uint8):
+        assert needed(monkeypatch, "mmq_moe_plan", kind(64), 512, kind(8), 0, 0) == want
