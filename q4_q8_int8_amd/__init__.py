@@ -760,7 +760,10 @@ def q4G_format(group: int, scale_dtype, zeros: bool) -> mmq_q4G_format:
     zero) of scale_dtype, torch.float16 or torch.bfloat16."""
     if scale_dtype not in (torch.float16, torch.bfloat16):
         raise MMQArgumentError(f"scale_dtype: must be float16 or bfloat16, got {scale_dtype}")
-    return mmq_q4G_format(_int(group), TYPES[scale_dtype], int(bool(zeros)), 0)
+    group = _int(group)
+    if not -2 ** 31 <= group < 2 ** 31:  # the structure would keep its low 32 bits
+        raise MMQArgumentError(f"group: {group} does not fit 32 bits")
+    return mmq_q4G_format(group, TYPES[scale_dtype], int(bool(zeros)), 0)
 
 
 @_sizes
