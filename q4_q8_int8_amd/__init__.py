@@ -634,7 +634,8 @@ def moe_groups(groups, M: int, E: int, k: int):
     """Views (offsets [E + 1], order [M*k], place [M*k]) of what mmq_moe_group wrote."""
     M, E, k = _int(M), _int(E), _int(k)
     need = _group_sizes(M, E, k)[1]
-    if groups.dtype != torch.int32 or not groups.is_contiguous() or groups.nbytes < need:
+    if (not isinstance(groups, torch.Tensor) or groups.dtype != torch.int32
+            or not groups.is_contiguous() or groups.nbytes < need):
         raise MMQArgumentError(f"groups: must be a contiguous int32 tensor of {need} bytes or more")
     P, at = M * k, groups.storage_offset()
     a = (E + 1 + 3) // 4 * 4
@@ -776,6 +777,8 @@ def _q4G_bytes(N, K, group, scale_type, zeros, reserved):
 
 
 def _q4G_size(N, K, f):
+    if not isinstance(f, mmq_q4G_format):
+        raise MMQArgumentError(f"format: expected an mmq_q4G_format, got {type(f).__name__}")
     return _q4G_bytes(N, K, f.group, f.scale_type, f.zeros, f.reserved)
 
 

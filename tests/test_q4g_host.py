@@ -19,3 +19,15 @@ def test_a_group_that_the_format_cannot_hold():
     for group in (2 ** 31, 2 ** 32 + 64, 2 ** 63 - 1, 2 ** 64 + 32, -2 ** 32 + 32):
         with pytest.raises(mmq.MMQArgumentError):
             mmq.q4G_format(group, torch.float16, False)
+
+
+def test_other_kinds_of_arguments_are_refused():
+    f32 = types.SimpleNamespace(dtype=torch.float32)
+    for call in (lambda: mmq.moe_groups(None, 3, 8, 2),
+                 lambda: mmq.moe_groups(np.zeros(28, np.int32), 3, 8, 2),
+                 lambda: mmq.mmq_q4G_repacked_bytes(16, 96, None),
+                 lambda: mmq.mmq_q4G_repacked_bytes(16, 96, (32, 1, 0, 0)),
+                 lambda: mmq.mmq_q4G(1, 16, 96, f32, None, None, f32),
+                 lambda: mmq.repack_q4_G(None, None, None, 16, 96, None, None)):
+        with pytest.raises(mmq.MMQArgumentError):
+            call()
