@@ -7,7 +7,11 @@
 // of activations, src1 16 weight rows, so a lane's four results are of one weight row and share its
 // scale. Every product is exact in float32: a nibble is exact in f16; for bf16 the operand is 16 + v
 // (the bits of 16 with v in the upper mantissa bits, one AND-OR behind a shift), and the 16 goes out
-// with the zero, - (16 + z) sum x. A float16 or bfloat16 token is one column, token t being column
+// with the zero, - (16 + z) sum x. That operand and the ones below come with a factor of 2^-12, which
+// an output's sum is freed of at its end: 128 x 31 x 2^-12 is below 1, so that no sum of a record
+// overflows where its terms, of either sign and larger than those of v - z, would, whatever finite
+// values a token has (the bits are those without the factor, but for sums below 2^-114, which get an
+// error of 2^-137 for each of their terms). A float16 or bfloat16 token is one column, token t being column
 // 4 (t % 4) + t / 4, so that up to four tokens need one result register. A float32 token is three
 // columns, its values' three bf16 pieces, which sum to them exactly (bf16_trunc3): token t has columns
 // 4 (t % 4) .. + 2 of column tile t / 4, so that its three sums meet in one lane. sum x is the same
@@ -65,12 +69,15 @@ __device__ __forceinline__ uint32_t keep(uint32_t v) {
   return v;
 }
 
-// The eight values of a dword as the matrix operand, four registers of two: v for f16, 16 + v for bf16.
+// The eight values of a dword as the matrix operand, four registers of two: v for f16, 2^-12 (16 + v) for
+// bf16, and the 1 (2^-12) that sums x.
 template <bool BF>
 struct Unpack;
 template <>
 struct Unpack<true> {
-  uint32_t sixteen = keep(0x41804180u);
+  static constexpr uint32_t kOne = 0x39803980u;  // 2^-12
+  static constexpr float kOffset = 16.0f, kUnit = 0x1p12f;  // what it has above v; the factor back
+  uint32_t sixteen = keep(0x3B803B80u);  // 2^-12 x 16
   __device__ __forceinline__ v4u operator()(uint32_t w) const {
     constexpr uint32_t mask = 0x00780078u;
     return v4u{((w << 3) & mask) | sixteen, ((w >> 1) & mask) | sixteen,
@@ -79,6 +86,8 @@ struct Unpack<true> {
 };
 template <>
 struct Unpack<false> {
+  static constexpr uint32_t kOne = 0x3C003C00u;
+  static constexpr float kOffset = 0.0f, kUnit = 1.0f;
   // 0x6400 | v is 1024 + v and 0x5400 | v << 4 is 64 + v, exactly
   uint32_t big = keep(0x64006400u), mid = keep(0x54005400u);
   __device__ __forceinline__ v4u operator()(uint32_t w) const {
@@ -269,9 +278,8 @@ __global__ __launch_bounds__(64 * max_waves(XT, Q)) void q4g_kernel(
 
   float out[Q];
   const Unpack<BF> unpack;
-  const uint32_t one = BF ? 0x3F803F80u : 0x3C003C00u;
+  constexpr uint32_t one = Unpack<BF>::kOne;
   const v4u ones = v4u{keep(one), keep(one), keep(one), keep(one)};
-  constexpr float kOffset = BF ? 16.0f : 0.0f;  // what the operand has above v
 
   auto compute = [&](const Weights& r, const uint8_t* xj) {
     v4f acc[CT], xs[CT];
@@ -289,7 +297,7 @@ __global__ __launch_bounds__(64 * max_waves(XT, Q)) void q4g_kernel(
       if (last) {
         const int g = m / (4 / S);
         const float sc = r.s.template get<SBF>(g);
-        const float z = kOffset + (zeros ? r.z.template get<SBF>(g) : 8.0f);
+        const float z = Unpack<BF>::kOffset + (zeros ? r.z.template get<SBF>(g) : 8.0f);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
           float a, b;
@@ -377,6 +385,7 @@ __global__ __launch_bounds__(64 * max_waves(XT, Q)) void q4g_kernel(
       const float* r = red + b * nw * kSums + e;
       float v = r[0];
       for (int k = 1; k < nw; ++k) v += r[k * kSums];
+      v *= Unpack<BF>::kUnit;
       if (epi.bias) v += epi.bias[j];
       v = activate(v, epi.act);
       const size_t at = (size_t)t * N + j;

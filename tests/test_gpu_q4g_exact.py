@@ -1,6 +1,6 @@
 """Matrix-vector products with group scales where the result is known to a rounding: one value in each
 token that is not 0, in every place of a record and for every number of tokens, with x on every way into
-LDS.
+LDS; and finite tokens of any size, up to the greatest float.
 """
 import numpy as np
 import pytest
@@ -87,3 +87,40 @@ def test_one_value_each(N, K, group, counts, x):
                 lu.assert_close(got, used * (v - z), qu.one_value_bound(used, v, z), what=str(at))
             else:   # at most 11 and 4 bits
                 assert np.array_equal(got, used * (v - z)), at
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K", [(35, 160), (4200, 160), (35, 8192)])
+def test_one_value_of_any_size(N, K, x):
+    """Up to the greatest float of the type; the results, 2^-6 x (v - z), are finite."""
+    m = Matrix(N, K, 32, s=2.0 ** -6, seed=3)
+    greatest = torch.finfo(DT[x]).max
+    for M in (1, 3, 9, 16):
+        at = np.random.default_rng(M).permutation(K)[:M]
+        for size in (1e35, 1e36, 1e37, 1e38, greatest):
+            say("q4_G, one value of", size, (M, N, K), x)
+            a = one_value_each(np.where(np.arange(M) % 2, -size, size), at, K, x)
+            used = np64(a)[np.arange(M), at][:, None]
+            v, z = m.v[:, at].T, m.zeros[:, at].T
+            lu.assert_close(m(a), used * (v - z) / 64, qu.one_value_bound(used, v, z) / 64)
+
+
+@pytest.mark.parametrize("x,size", [("f32", 1e34), ("f32", 3e38), ("bf16", 1e34), ("bf16", 3e38),
+                                    ("f32", 2.0 ** -110), ("f32", 2.0 ** -124),
+                                    ("bf16", 2.0 ** -110), ("bf16", 2.0 ** -124),
+                                    ("f16", 6e4), ("f16", 2.0 ** -23)])
+def test_tokens_of_any_size(x, size):
+    """Every value of a token of this size, in groups of a record and of several. What is below 2^-126
+    after the operands' factor of 2^-12 is rounded to 2^-149, a unit per sum of a piece's products
+    with 16 + v (at most 31) or with 1 (taken 16 + z times, at most 31): 2^-137 each in the result,
+    which is 4096 times as large."""
+    for K, group in ((512, 128), (1056, 1056)):
+        m = Matrix(33, K, group, s=2.0 ** -14 if size > 1 else 1.0, scale="bf16", seed=5)
+        g = torch.Generator().manual_seed(K)
+        for M in (2, 4, 11):
+            a = ((torch.rand(M, K, generator=g) + 0.1).clamp(max=1.0) * size
+                 * torch.where(torch.rand(M, K, generator=g) < 0.5, -1.0, 1.0)).to(DT[x]).cuda()
+            say("q4_G, tokens of", size, x, (M, K))
+            y, T = m.product(a)
+            least = 0.0 if x == "f16" else 3 * (1 + 31) * K * 2.0 ** -137 * m.size
+            lu.assert_close(m(a), y, qo.bound(T, K) + least + 2.0 ** -149)
