@@ -1,5 +1,6 @@
 """The products grouped by expert where there is little or nothing sensible to do, in every form of the
-kernel: no pair with an expert, groups of nonsense, experts without rows between ragged ones.
+kernel: no pair with an expert, groups of nonsense, experts without rows between ragged ones; and the
+layer of many tokens against the one of a few.
 """
 import numpy as np
 import pytest
@@ -202,3 +203,61 @@ def test_ragged_experts_in_the_wide_gated_form(k):
                                act=mmq.MMQ_ACT_SILU, force_tile=mmq.MMQ_TILE_LARGE)
         assert torch.equal(H[ps], want), e
     assert bool(torch.isnan(H[torch.from_numpy(np.nonzero(flat < 0)[0]).cuda()]).all())
+
+
+@pytest.mark.parametrize("M,E,k,D,F", [(64, 8, 2, 512, 768), (61, 4, 3, 300, 512),
+                                       (9, 16, 8, 256, 256), (1, 4, 2, 256, 512)])
+def test_the_layer_of_many_tokens_against_that_of_a_few(M, E, k, D, F):
+    """Both gated products within their bound of one oracle; both down products, on either's H, within
+    the sum of their bounds of each other; and both layers are their own calls, bit for bit."""
+    K = -(-D // 256) * 256      # the tokens' width
+    gate, up = ([lu.weights(F, K, s + e) for e in range(E)] for s in (700, 900))
+    ws = np.stack([lu.weights(D, F, 800 + e) for e in range(E)])
+    n, m = mmq.mmq_q4K_pair_bytes(F, K), mmq.mmq_q4K_repacked_bytes(D, F)
+    pairs, down = raw(E * n), raw(E * m)
+    for e in range(E):
+        mmq.repack_q4_K_pair(to_dev(gate[e]), to_dev(up[e]), F, K, pairs[e * n:(e + 1) * n])
+        mmq.repack_q4_K(to_dev(ws[e]), D, F, down[e * m:(e + 1) * m])
+    xh = synth.activations("normal_outliers", M, K, 1)
+    rng = np.random.default_rng(2)
+    logits = rng.standard_normal((M, E)).astype(np.float32)
+    logits[M // 2] = -np.inf if M > 1 else logits[0]
+    residual = rng.standard_normal((M, D)).astype(np.float32)
+    x, lg, res = to_dev(xh), to_dev(logits), to_dev(residual)
+    ids, w = torch.empty(M, k, dtype=torch.int32, device="cuda"), f32(M, k)
+    plan = torch.zeros(mmq.mmq_moe_plan_bytes(M, E, k) // 4, dtype=torch.int32, device="cuda")
+    say("layers of many and of a few", (M, E, k, D, F))
+    mmq.mmq_moe_route(M, E, k, lg, ids, w, plan=plan)
+    torch.cuda.synchronize()
+    idh, wh = ids.cpu().numpy(), w.cpu().numpy()
+    g = group(idh, E)
+    H = {"few": f32(M * k, F, value=0.0), "many": f32(M * k, F, value=0.0)}
+    q8 = raw(max(mmq.mmq_q8_1_bytes(M, K), mmq.mmq_q8_1_bytes(M * k, F)))
+    mmq.mmq_q4K_moe_gated(M, E, k, F, K, x, plan, pairs, H["few"], q8)
+    mmq.mmq_q4K_grouped_gated(M, E, k, F, K, x, g, pairs, H["many"], q8)
+    want, err = lu.experts_gated(xh, idh, np.stack(gate), np.stack(up), "silu")
+    used = idh.reshape(-1) >= 0
+    got = {name: t.cpu().numpy() for name, t in H.items()}
+    for name in H:
+        lu.assert_close(got[name][used], want[used], err[used], what=name)
+    lu.assert_close(got["few"][used], got["many"][used].astype(np.float64), 2 * err[used])
+    space = raw(mmq.mmq_grouped_down_workspace_bytes(M, E, k, D, F))
+    last = {}
+    for name, h in H.items():
+        few, many = f32(M, D), f32(M, D)
+        mmq.mmq_q4K_moe_down(M, E, k, D, F, h, plan, w, down, few, q8, residual=res)
+        mmq.mmq_q4K_grouped_down(M, E, k, D, F, h, g, w, down, many, space, residual=res)
+        torch.cuda.synchronize()
+        out, oerr = lu.experts_down(got[name], idh, wh, ws, residual)
+        lu.assert_close(few.cpu().numpy(), out, oerr)
+        lu.assert_close(many.cpu().numpy(), out, oerr)
+        lu.assert_close(few.cpu().numpy(), many.double().cpu().numpy(), 2 * oerr)
+        last[name] = few if name == "few" else many
+    if K == D:      # the layers take one width
+        few, many = f32(M, D), f32(M, D)
+        mmq.mmq_q4K_moe(M, E, k, D, F, x, lg, pairs, down, few,
+                        raw(mmq.mmq_moe_workspace_bytes(M, E, k, D, F)), residual=res)
+        mmq.mmq_q4K_grouped_moe(M, E, k, D, F, x, lg, pairs, down, many,
+                                raw(mmq.mmq_grouped_moe_workspace_bytes(M, E, k, D, F)),
+                                residual=res)
+        assert torch.equal(few, last["few"]) and torch.equal(many, last["many"])
