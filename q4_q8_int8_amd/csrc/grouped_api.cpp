@@ -201,7 +201,7 @@ int mmq_q4K_grouped(int64_t M, int64_t E, int64_t k, int64_t N, int64_t K, const
                     int32_t act, void* stream) {
   int st = check_groups(M, E, k);
   if (!st && per_pair != 0 && per_pair != 1) st = fail(MMQ_E_ARG, "per_pair must be 0 or 1");
-  const int64_t rows = per_pair ? M * k : M;
+  const int64_t rows = !st && per_pair ? M * k : M;
   if (!st) st = check_product(M, E, k, "N", N, false, "K", K, rows);
   if (!st) st = check_act(act);
   if (!st) st = check_pointers({x, groups, w_rep, C, q8});

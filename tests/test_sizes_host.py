@@ -102,3 +102,12 @@ def test_size_of_a_plans_ids(monkeypatch):
     assert want["ids"] == 4 * 64 * 8
     for kind in (np.int8, np.uint8):
         assert needed(monkeypatch, "mmq_moe_plan", kind(64), 512, kind(8), 0, 0) == want
+
+
+def test_sizes_are_not_multiplied_before_they_are_checked():
+    """The rows of x per pair, M k, would pass 64 bits."""
+    p = 1 << 20
+    for per_pair in (0, 1, 2):
+        for M, k in ((1 << 62, 8), (2 ** 63 - 1, 64), (-(1 << 62), 8)):
+            assert mmq.raw_call("mmq_q4K_grouped", M, 64, k, 64, 256, p, per_pair, p, p, p, p, 0,
+                                None) == (mmq.MMQ_E_SHAPE if M > 0 else mmq.MMQ_E_ARG)
