@@ -91,7 +91,7 @@ int check_gated(int64_t M, int64_t E, int64_t k, int64_t F, int64_t D, int32_t a
   if (!st) st = check_act(act);
   // at most two workgroups of 256 work-items per (expert, 16 columns), on a 1-D grid of fewer than
   // 2^32 work-items
-  const int64_t entries = mmq::MoeShape{M, E, k, D, F}.entries();
+  const int64_t entries = st ? 0 : mmq::MoeShape{M, E, k, D, F}.entries();
   if (!st && (F + 15) / 16 * entries >= ((int64_t)1 << 23))
     st = fail(MMQ_E_SHAPE, "min(E, M*k) * ceil(F/16) = %lld is not below 2^23",
               (long long)((F + 15) / 16 * entries));

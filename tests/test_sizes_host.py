@@ -2,6 +2,7 @@
 a narrow integer, a numpy one or a 0-d tensor, is not multiplied in its own width, where the product
 would wrap and let a short buffer through.
 """
+import ctypes
 import types
 
 import numpy as np
@@ -111,3 +112,15 @@ def test_sizes_are_not_multiplied_before_they_are_checked():
         for M, k in ((1 << 62, 8), (2 ** 63 - 1, 64), (-(1 << 62), 8)):
             assert mmq.raw_call("mmq_q4K_grouped", M, 64, k, 64, 256, p, per_pair, p, p, p, p, 0,
                                 None) == (mmq.MMQ_E_SHAPE if M > 0 else mmq.MMQ_E_ARG)
+
+
+def test_a_plans_sizes_are_not_multiplied_before_they_are_checked():
+    p = 1 << 20
+    for M, E, k in ((2 ** 63 - 1, 8, 8), (1 << 40, 1 << 40, 1 << 40), (1, 8, 2 ** 63 - 1)):
+        sizes = (M, E, k, 256, 256)
+        assert mmq.raw_call("mmq_q4K_moe_gated", *sizes, p, p, p, p, p, 2, None) == mmq.MMQ_E_SHAPE
+        assert mmq.raw_call("mmq_q4K_moe_down", *sizes, p, p, p, p, None, p, p, None) == mmq.MMQ_E_SHAPE
+        assert mmq.raw_call("mmq_moe_plan", M, E, k, p, p, None) == mmq.MMQ_E_SHAPE
+        assert mmq.raw_call("mmq_moe_route", M, E, k, p, 0, 1, p, p, p, None) == mmq.MMQ_E_SHAPE
+        assert mmq.raw_call("mmq_moe_workspace_bytes", *sizes,
+                            ctypes.byref(ctypes.c_size_t())) == mmq.MMQ_E_SHAPE
