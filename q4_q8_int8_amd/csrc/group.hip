@@ -11,9 +11,10 @@
 //
 // Bound by latency: reads of the ids, LDS round trips and launches. Up to 4096 pairs one workgroup does it
 // (graph replays, a launch being 3.6 us: 800 pairs 3.7 us, 2000 4.7, 4096 6.5); above, chunks of 2048 pairs in
-// two kernels (4100 pairs 7.6 us, 16384 8.1, 65536 of 256 experts 9.3, 2^21 90), which take as long as that for
-// fewer pairs too. Chunks of 4096 with the counts added up by one work-item per expert and the ranks found
-// twice took 12.4 us for the 65536.
+// two kernels (4100 pairs 7.6 us, 16384 8.1, 65536 of 256 experts 9.3, 2^21 86, 2^21 of 512 experts 153: every
+// workgroup of the second reads the counts of all chunks), which take as long as that for fewer pairs too.
+// Chunks of 4096 with the counts added up by one work-item per expert and the ranks found twice took 12.4 us for
+// the 65536.
 #include "grouped_internal.h"
 
 namespace mmq {

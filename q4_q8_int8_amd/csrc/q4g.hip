@@ -24,7 +24,11 @@
 // wavefront brings the values of x for its own records into LDS with its first tile, in the form of the
 // operands: read from memory for every tile they take more of the vector memory unit than the weights do,
 // and their latency is not covered (16 tokens, 11008 x 4096: 16.3 us in a graph, 11.5 from LDS). Beside the
-// loads, unpacking counts: 9 vector instructions per 8 values for f16 and 8 for bf16.
+// loads, unpacking counts: 9 vector instructions per 8 values for f16 and 8 for bf16. Where x of a wavefront's
+// records does not fit the LDS it is brought in for one record at a time, anew for every tile, behind a wait that
+// the weights in flight end with too: 16 x 8192 x 8192 bf16 15.7 us (36 MB), 16 x 28672 x 8192 46.9 (125 MB); for
+// float32 tokens from 7 on at K = 4096, 16 x 11008 x 4096 24.5 (24 MB). With 9 float32 tokens or more and four
+// scales a record the kernel spills 57 registers with x in LDS, 2 without (27.6 us).
 //
 // Graph replays over weights beyond the caches, a launch being 3.6 us of each: 1 x 4096 x 4096 f16 5.1 us (9 MB),
 // 1 x 4096 x 11008 f32 with groups of 32 and zeros 11.1 (28 MB), 16 x 11008 x 4096 bf16 11.4 (24 MB),
