@@ -7,9 +7,10 @@
  *   y[i][j] = act( sum_k x_ik w_jk + bias_j ) + residual_ij
  *
  * Activations are float32, float16 or bfloat16 and are not quantized: every product x v is exact in
- * float32, all sums are float32, and a result is rounded once, to the output's type. For zeros in
- * 0..16 no sum overflows on the way to a result that float32 holds, however large the (finite) values
- * of x. Products and sums below 2^-114 s are exact to 2^-137 s each, s being the scale.
+ * float32, all sums are float32, and a result is rounded once, to the output's type. No sum over 128
+ * values overflows, whatever finite values x has, for zeros in 0..16, and none over a row while its
+ * partial sums are below 2^128 (float32 and bfloat16 x: 2^140). Products and sums below 2^-114 s are
+ * exact to 2^-137 s each, s being the scale.
  *
  * The conventions of mmq.h hold: DEVICE pointers owned by the caller, 16-byte aligned, not
  * overlapping (but for a residual that is the output); `stream` is a hipStream_t; every argument is
